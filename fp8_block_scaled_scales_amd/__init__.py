@@ -39,6 +39,8 @@ DG_IN_F16 = 2
 DG_ACT_NONE = 0
 DG_ACT_RELU = 1
 DG_ACT_GELU = 2
+DG_ACT_SILU = 3
+DG_ACT_GELU_TANH = 4
 DG_MAX_DIM = (1 << 24) - 256  # largest M, N or K (and quantiser rows, cols) the library accepts
 
 
@@ -96,6 +98,22 @@ def load_library(path: str):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [vp, ctypes.c_int, i64, i64, ctypes.c_int, ctypes.c_int, vp, vp, vp]
+    fmt, act, kind, f32 = ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float
+    lib.dg_gemm_fp8_residual.restype = ctypes.c_int
+    lib.dg_gemm_fp8_residual.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                         fmt, fmt, vp, act, vp, kind, i64, vp, vp]
+    lib.dg_rmsnorm_quantize_fp8.restype = ctypes.c_int
+    lib.dg_rmsnorm_quantize_fp8.argtypes = [vp, kind, i64, vp, kind, i64, vp, f32, i64, i64, ctypes.c_int, fmt, vp, vp,
+                                            vp, vp, vp, vp]
+    lib.dg_rmsnorm_backward.restype = ctypes.c_int
+    lib.dg_rmsnorm_backward.argtypes = [vp, kind, i64, vp, kind, i64, vp, vp, vp, i64, i64, i64, vp, vp, vp, i64, vp]
+    lib.dg_rmsnorm_backward_workspace.restype = i64
+    lib.dg_rmsnorm_backward_workspace.argtypes = [i64, i64]
+    lib.dg_epilogue_backward_fp8.restype = ctypes.c_int
+    lib.dg_epilogue_backward_fp8.argtypes = [vp, kind, i64, vp, i64, act, i64, i64, ctypes.c_int, ctypes.c_int, fmt, vp,
+                                             vp, vp, vp, vp, i64, vp]
+    lib.dg_epilogue_backward_workspace.restype = i64
+    lib.dg_epilogue_backward_workspace.argtypes = [i64, i64, ctypes.c_int, ctypes.c_int]
     lib.dg_strerror.restype = ctypes.c_char_p
     lib.dg_strerror.argtypes = [ctypes.c_int]
     lib.dg_version.restype = ctypes.c_int
@@ -302,8 +320,9 @@ def dg_workspace(M: int, N: int, K: int, gran: int = 128, layout: int = DG_LAYOU
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
-def _ws_args(a, b, sa, sb, out, gran, layout, sa_rows, fmt_a, fmt_b, bias, act):
-    """Checks shared by dg_gemm_fp8_ws and dg_gemm_fp8_noalloc; returns (M, N, K, sa_rows, dev)."""
+def _ws_args(a, b, sa, sb, out, gran, layout, sa_rows, fmt_a, fmt_b, bias, act, more=None):
+    """Checks shared by the calls that take a layout with sa_rows; returns (M, N, K, sa_rows, dev).
+    more(M, N, dev): a call's further checks."""
     if layout not in (DG_LAYOUT_NT, DG_LAYOUT_NN, DG_LAYOUT_TT, DG_LAYOUT_TN):
         raise ValueError("layout must be DG_LAYOUT_NT, _NN, _TT or _TN")
     if a.dim() != 2 or b.dim() != 2:
@@ -328,6 +347,8 @@ def _ws_args(a, b, sa, sb, out, gran, layout, sa_rows, fmt_a, fmt_b, bias, act):
         _check(bias, "bias", (torch.float32,), (N,), dev)
     if act not in (DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU):
         raise ValueError("act must be DG_ACT_NONE, DG_ACT_RELU or DG_ACT_GELU")
+    if more is not None:
+        more(M, N, dev)
     if dev.type != "cuda":
         raise ValueError("a must be a GPU tensor")
     return M, N, K, sa_rows, dev
@@ -463,10 +484,232 @@ def dg_quantize_fp8_rows_typed(x, gran: int = 128, fmt: int = DG_FMT_E4M3, q=Non
     return _quantize(x, gran, fmt, q, scales, stream, "dg_quantize_fp8_rows_typed")
 
 
+# ---- the operators around the product in a transformer layer ----------------
+
+_F32 = (torch.float32,)
+_BF16 = (torch.bfloat16,)
+
+
+def _rows(t, name, dtypes, rows, cols, dev):
+    """Checks an input matrix whose rows may lie apart (a slice of a wider one); its row pitch in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in dtypes:
+        raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, tuple(dtypes)))
+    if t.shape != (rows, cols):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, cols)))
+    pitch, step = t.stride()
+    if (step != 1 and cols > 1) or (pitch < cols and rows > 1):
+        raise ValueError("%s must have contiguous rows that do not overlap" % name)
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    return pitch if rows > 1 else cols
+
+
+def _out(t, name, dtypes, shape, dev, stream):
+    """Checks an output, or allocates it on the call's stream."""
+    if t is not None:
+        _check(t, name, dtypes, shape, dev)
+        return t
+    if stream is None:
+        return torch.empty(shape, dtype=dtypes[-1], device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtypes[-1], device=dev)
+
+
+def _workspace(t, nbytes, dev, stream):
+    """(pointer, bytes) of a call's workspace: the caller's, or one from torch's allocator on the call's stream
+    (returned too, so that it lives until the launch)."""
+    if not nbytes:
+        return None, None, 0
+    if t is None:
+        t = _out(None, "workspace", (torch.uint8,), (nbytes,), dev, stream)
+    else:
+        _check(t, "workspace", (torch.uint8,), (t.numel(),), dev)
+    return t, t.data_ptr(), t.numel()
+
+
+def _launch(fn, where, dev, stream, *args):
+    """Calls fn(*args, stream) with dev current; a status other than DG_OK raises."""
+    if dev.type != "cuda":
+        raise ValueError("%s needs GPU tensors" % where)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s.cuda_stream)
+    if rc != DG_OK:
+        _raise(rc, where)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor" % name)
+    return t.shape[0], t.shape[1], t.device
+
+
+def dg_gemm_fp8_residual(a, b, sa, sb, res=None, out=None, gran: int = 128, layout: int = DG_LAYOUT_NT,
+                         sa_rows: int | None = None, fmt_a: int = DG_FMT_E4M3, fmt_b: int = DG_FMT_E4M3, bias=None,
+                         act: int = DG_ACT_NONE, pre=None, stream=None):
+    """out = bf16(act(C + bias) + res), the product with a residual and any activation in its epilogue.
+
+    a, b, sa, sb, gran, layout, sa_rows, formats and bias as dg_gemm_fp8_ws. res: [M,N]
+    float32, bfloat16 or float16, rows contiguous (any pitch), or None; it may be out
+    itself. act: one of the five DG_ACT_* codes. pre: optional [M,N] bfloat16 that
+    receives C + bias, for dg_epilogue_backward_fp8.
+    """
+    if act not in (DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU, DG_ACT_SILU, DG_ACT_GELU_TANH):
+        raise ValueError("act must be one of the DG_ACT_* codes")
+    kind, pitch = 0, 0
+
+    def more(M, N, dev):
+        nonlocal kind, pitch
+        if res is not None:
+            pitch = _rows(res, "res", _IN_OF, M, N, dev)
+            kind = _IN_OF[res.dtype]
+        if pre is not None:
+            _check(pre, "pre", _BF16, (M, N), dev)
+
+    M, N, K, sa_rows, dev = _ws_args(a, b, sa, sb, out, gran, layout, sa_rows, fmt_a, fmt_b, bias, DG_ACT_NONE, more)
+    if out is None:
+        out = _out(None, "out", _BF16, (M, N), dev, stream)
+    _launch(_lib.dg_gemm_fp8_residual, "dg_gemm_fp8_residual", dev, stream, a.data_ptr(), b.data_ptr(), sa.data_ptr(),
+            sb.data_ptr(), out.data_ptr(), M, N, K, gran, layout, sa_rows, fmt_a, fmt_b, _ptr(bias), act, _ptr(res),
+            kind, pitch, _ptr(pre))
+    return out
+
+
+def dg_rmsnorm_quantize_fp8(x, res, weight, eps: float = 1e-6, gran: int = 128, fmt: int = DG_FMT_E4M3, h=None, y=None,
+                            rstd=None, q=None, scales=None, stream=None):
+    """(q, scales, h): h = x + res, its RMS norm times weight, quantised with one factor per row and gran-wide segment.
+
+    x: [rows, cols] float32, bfloat16 or float16; res: the residual stream, likewise
+    (either may have a row pitch), or None, and then h is x. weight: [cols] float32.
+    h: optional output of res's dtype (may be res). y (x's dtype) and rstd ([rows]
+    float32), where given, receive the normed values and 1 / rms, which
+    dg_rmsnorm_backward and the weight gradient's product need. q (uint8 holding fmt's
+    codes, or that float8 dtype) and scales [rows, cols/gran] are what
+    dg_gemm_fp8_residual takes as a and sa with sa_rows = 1.
+    """
+    rows, cols, dev = _matrix(x, "x")
+    if gran not in _GRANS or cols % gran:
+        raise ValueError("gran must be 64, 128 or 256 and divide cols")
+    if fmt not in _FP8_OF:
+        raise ValueError("fmt must be DG_FMT_E4M3 or DG_FMT_E5M2")
+    ldx = _rows(x, "x", _IN_OF, rows, cols, dev)
+    _check(weight, "weight", _F32, (cols,), dev)
+    rk, ldres = 0, 0
+    if res is not None:
+        ldres = _rows(res, "res", _IN_OF, rows, cols, dev)
+        rk = _IN_OF[res.dtype]
+        h = _out(h, "h", (res.dtype,), (rows, cols), dev, stream)
+    elif h is not None:
+        raise ValueError("h is written only where there is a residual")
+    if y is not None:
+        _check(y, "y", (x.dtype,), (rows, cols), dev)
+    if rstd is not None:
+        _check(rstd, "rstd", _F32, (rows,), dev)
+    q = _out(q, "q", _FP8_OF[fmt], (rows, cols), dev, stream)
+    scales = _out(scales, "scales", _F32, (rows, cols // gran), dev, stream)
+    _launch(_lib.dg_rmsnorm_quantize_fp8, "dg_rmsnorm_quantize_fp8", dev, stream, x.data_ptr(), _IN_OF[x.dtype], ldx,
+            _ptr(res), rk, ldres, weight.data_ptr(), eps, rows, cols, gran, fmt, _ptr(h), _ptr(y), _ptr(rstd),
+            q.data_ptr(), scales.data_ptr())
+    return q, scales, x if res is None else h
+
+
+def dg_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None, stream=None):
+    """(dx, dweight): the gradient of dg_rmsnorm_quantize_fp8's norm, from dy, the gradient of y.
+
+    h, rstd, weight: as the forward pass left them. dh: the gradient that reaches the
+    stream h past the norm (h's dtype), added to dx; dx may be dh. dx is the gradient
+    of x and of the residual alike, of h's dtype; dweight is [cols] float32. workspace:
+    a uint8 tensor of dg_rmsnorm_backward_workspace(rows, cols) bytes (allocated when None).
+    """
+    rows, cols, dev = _matrix(dy, "dy")
+    if cols % 64 or not rows or not cols:
+        raise ValueError("dy must have rows, and columns in a multiple of 64")
+    lddy = _rows(dy, "dy", _IN_OF, rows, cols, dev)
+    ldh = _rows(h, "h", _IN_OF, rows, cols, dev)
+    _check(rstd, "rstd", _F32, (rows,), dev)
+    _check(weight, "weight", _F32, (cols,), dev)
+    lddh = 0 if dh is None else _rows(dh, "dh", (h.dtype,), rows, cols, dev)
+    dx = _out(dx, "dx", (h.dtype,), (rows, cols), dev, stream)
+    dweight = _out(dweight, "dweight", _F32, (cols,), dev, stream)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, dg_rmsnorm_backward_workspace(rows, cols), dev, stream)
+    _launch(_lib.dg_rmsnorm_backward, "dg_rmsnorm_backward", dev, stream, dy.data_ptr(), _IN_OF[dy.dtype], lddy,
+            h.data_ptr(), _IN_OF[h.dtype], ldh, rstd.data_ptr(), weight.data_ptr(), _ptr(dh), lddh, rows, cols,
+            dx.data_ptr(), dweight.data_ptr(), ws_ptr, ws_bytes)
+    return dx, dweight
+
+
+def dg_rmsnorm_backward_workspace(rows: int, cols: int) -> int:
+    """Workspace bytes of dg_rmsnorm_backward."""
+    n = _lib.dg_rmsnorm_backward_workspace(rows, cols)
+    if n < 0:
+        _raise(n, "dg_rmsnorm_backward_workspace")
+    return n
+
+
+def dg_epilogue_backward_fp8(dout, pre, act: int, gran: int = 128, block_rows: int | None = None,
+                             fmt: int = DG_FMT_E5M2, dz=None, dbias=None, q=None, scales=None, workspace=None,
+                             stream=None):
+    """(q, scales): dz = dout * act'(pre) as FP8 codes with factors, the gradient through the product's epilogue.
+
+    dout: [rows, cols] float32, bfloat16 or float16; pre: the bfloat16 pre-activation
+    dg_gemm_fp8_residual kept (None with DG_ACT_NONE). block_rows: gran (gran x gran
+    blocks, the default: the codes serve both following products) or 1 (a factor per
+    row and segment). dz (dout's dtype; may be dout) and dbias ([cols] float32), where
+    given, receive the FP32 gradient rounded once and its sum over the rows.
+    workspace: a uint8 tensor of dg_epilogue_backward_workspace(...) bytes (allocated when None).
+    """
+    rows, cols, dev = _matrix(dout, "dout")
+    if gran not in _GRANS or cols % gran or not rows or not cols:
+        raise ValueError("dout must have rows and columns, and gran must be 64, 128 or 256 and divide cols")
+    if fmt not in _FP8_OF:
+        raise ValueError("fmt must be DG_FMT_E4M3 or DG_FMT_E5M2")
+    block_rows = gran if block_rows is None else block_rows
+    if block_rows not in (gran, 1):
+        raise ValueError("block_rows must be gran (g x g blocks) or 1 (per-row factors)")
+    if act not in (DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU, DG_ACT_SILU, DG_ACT_GELU_TANH):
+        raise ValueError("act must be one of the DG_ACT_* codes")
+    if (act == DG_ACT_NONE) != (pre is None):
+        raise ValueError("pre goes with an activation, and only with one")
+    lddout = _rows(dout, "dout", _IN_OF, rows, cols, dev)
+    ldpre = 0 if pre is None else _rows(pre, "pre", _BF16, rows, cols, dev)
+    if dz is not None:
+        _check(dz, "dz", (dout.dtype,), (rows, cols), dev)
+    need = 0
+    if dbias is not None:
+        _check(dbias, "dbias", _F32, (cols,), dev)
+        need = dg_epilogue_backward_workspace(rows, cols, gran, block_rows)
+    q = _out(q, "q", _FP8_OF[fmt], (rows, cols), dev, stream)
+    scales = _out(scales, "scales", _F32, ((rows + block_rows - 1) // block_rows, cols // gran), dev, stream)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev, stream)
+    _launch(_lib.dg_epilogue_backward_fp8, "dg_epilogue_backward_fp8", dev, stream, dout.data_ptr(),
+            _IN_OF[dout.dtype], lddout, _ptr(pre), ldpre, act, rows, cols, gran, block_rows, fmt, _ptr(dz), _ptr(dbias),
+            q.data_ptr(), scales.data_ptr(), ws_ptr, ws_bytes)
+    return q, scales
+
+
+def dg_epilogue_backward_workspace(rows: int, cols: int, gran: int = 128, block_rows: int | None = None) -> int:
+    """Workspace bytes of dg_epilogue_backward_fp8 with dbias."""
+    n = _lib.dg_epilogue_backward_workspace(rows, cols, gran, gran if block_rows is None else block_rows)
+    if n < 0:
+        _raise(n, "dg_epilogue_backward_workspace")
+    return n
+
+
 __all__ = ["dg_gemm_fp8_nt", "dg_gemm_fp8_nt_fmt", "dg_gemm_fp8_nt_epi", "dg_gemm_fp8_nt_ex", "dg_gemm_fp8_layout",
            "dg_gemm_fp8_ws", "dg_workspace", "dg_gemm_fp8_noalloc", "dg_noalloc_scratch_bytes", "DG_ESCRATCH",
            "DG_LAYOUT_NT", "DG_LAYOUT_NN", "DG_LAYOUT_TT", "DG_LAYOUT_TN", "DG_ACT_NONE",
            "DG_ACT_RELU", "DG_ACT_GELU", "dg_quantize_e4m3_blocks", "dg_quantize_fp8_blocks", "dg_quantize_fp8_rows",
            "dg_quantize_fp8_blocks_typed", "dg_quantize_fp8_rows_typed", "DG_IN_F32", "DG_IN_BF16", "DG_IN_F16",
            "dg_query_tile", "dg_strerror", "dg_version", "DGError", "DGArgumentError", "DG_OK", "DG_EINVAL",
+           "dg_gemm_fp8_residual", "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward", "dg_rmsnorm_backward_workspace",
+           "dg_epilogue_backward_fp8", "dg_epilogue_backward_workspace", "DG_ACT_SILU", "DG_ACT_GELU_TANH",
            "DG_EALIGN", "DG_EUNSUPPORTED", "DG_ELAUNCH", "DG_FMT_E4M3", "DG_FMT_E5M2", "DG_MAX_DIM", "LIB_PATH"]

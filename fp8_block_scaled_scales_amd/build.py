@@ -15,9 +15,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg.so")
 # Longest compiles first, so the parallel build's slowest jobs start at once.
-SOURCES = ["gemm_fp8_big_layouts_rowa.hip", "gemm_fp8_big_layouts.hip", "gemm_fp8_stream.hip",
+SOURCES = ["gemm_fp8_big_layouts_rowa.hip", "gemm_fp8_big_layouts.hip", "gemm_fp8_residual.hip",
+           "gemm_fp8_residual_big_rowa.hip", "gemm_fp8_residual_big.hip", "gemm_fp8_stream.hip",
            "gemm_fp8_layouts_rowa.hip", "gemm_fp8_layouts.hip", "gemm_fp8_nt_big.hip", "gemm_fp8_nt.hip",
-           "quant_fp8.hip", "dg_host.hip"]
+           "epilogue_bwd.hip", "norm_fp8.hip", "quant_fp8.hip", "dg_host.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

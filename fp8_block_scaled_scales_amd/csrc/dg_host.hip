@@ -16,6 +16,7 @@
 
 #include "../../include/dg.h"
 #include "gemm_fp8_nt.h"
+#include "layer_ops.h"
 #include "quant_fp8.h"
 
 namespace {
@@ -237,19 +238,44 @@ bool overlaps(const void* p, uint64_t n, const void* q, uint64_t m) {
   return n && m && x < y + m && y < x + n;
 }
 
+// The residual epilogue's own arguments (dg_gemm_fp8_residual).
+struct Residual {
+  const void* res;
+  int res_type;
+  int64_t ldres;
+  void* pre;
+};
+
+// Bytes from the first element of a [rows][cols] matrix of row pitch ld to the
+// end of its last.
+uint64_t extent(int64_t rows, int64_t cols, int64_t ld, uint64_t esize) {
+  return esize * ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols);
+}
+
+bool known_kind(int type) { return type == DG_IN_F32 || type == DG_IN_BF16 || type == DG_IN_F16; }
+uint64_t kind_size(int type) { return type == DG_IN_F32 ? 4 : 2; }
+
+// A row pitch of an input: at least the row, at most DG_MAX_DIM.
+bool good_pitch(int64_t ld, int64_t cols) { return ld >= cols && ld <= DG_MAX_DIM; }
+
 // split_ok: few-tile long-K shapes may split K over workgroups, through ws (the
 // caller's, ws_bytes long; none when ws_bytes is 0) or, with use_scratch,
-// through the library's static scratch array.
+// through the library's static scratch array. rs: the residual epilogue (null:
+// none), which takes every activation and never splits.
 int gemm(const void* a, const void* b, const float* sa, const float* sb, void* out, int64_t M, int64_t N, int64_t K,
          int gran, int layout, int sa_rows, int fmt_a, int fmt_b, const float* bias, int act, void* stream,
-         bool split_ok = false, void* ws = nullptr, int64_t ws_bytes = 0, bool use_scratch = false) {
+         bool split_ok = false, void* ws = nullptr, int64_t ws_bytes = 0, bool use_scratch = false,
+         const Residual* rs = nullptr) {
   if (!a || !b || !sa || !sb || !out) return DG_EINVAL;
   if (sa_rows != gran && sa_rows != 1) return DG_EINVAL;
   if (validate_layout(M, N, layout) != DG_OK) return DG_EINVAL;
   if ((fmt_a != DG_FMT_E4M3 && fmt_a != DG_FMT_E5M2) || (fmt_b != DG_FMT_E4M3 && fmt_b != DG_FMT_E5M2))
     return DG_EINVAL;
-  if (act != DG_ACT_NONE && act != DG_ACT_RELU && act != DG_ACT_GELU) return DG_EINVAL;
+  if (act < DG_ACT_NONE || act > (rs ? DG_ACT_GELU_TANH : DG_ACT_GELU)) return DG_EINVAL;
+  if (rs && rs->res && (!known_kind(rs->res_type) || !good_pitch(rs->ldres, N))) return DG_EINVAL;
   if ((uintptr_t)bias & 3) return DG_EALIGN;
+  if (rs && (((uintptr_t)rs->pre & 1) || (rs->res && ((uintptr_t)rs->res & (kind_size(rs->res_type) - 1)))))
+    return DG_EALIGN;
   if (ws_bytes < 0 || (ws_bytes > 0 && !ws) || (ws && ws_bytes == 0)) return DG_EINVAL;
   if ((uintptr_t)ws & 255) return DG_EALIGN;
   int rc = validate(M, N, K, gran);
@@ -279,6 +305,17 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
     if (overlaps(ws, wsb, a, ab) || overlaps(ws, wsb, b, bb) || overlaps(ws, wsb, sa, sab) ||
         overlaps(ws, wsb, sb, sbb) || overlaps(ws, wsb, bias, biasb) || overlaps(ws, wsb, out, ob))
       return DG_EINVAL;
+    if (rs) {
+      // pre is an output like out. The residual may be out itself (BF16,
+      // pitch N): every element is read by the thread that then writes it.
+      const uint64_t rb = rs->res ? extent(M, N, rs->ldres, kind_size(rs->res_type)) : 0, pb = rs->pre ? ob : 0;
+      const bool in_place = rs->res == out && rs->res_type == DG_IN_BF16 && rs->ldres == N;
+      if (!in_place && overlaps(out, ob, rs->res, rb)) return DG_EINVAL;
+      if (overlaps(rs->pre, pb, out, ob) || overlaps(rs->pre, pb, rs->res, rb) || overlaps(rs->pre, pb, a, ab) ||
+          overlaps(rs->pre, pb, b, bb) || overlaps(rs->pre, pb, sa, sab) || overlaps(rs->pre, pb, sb, sbb) ||
+          overlaps(rs->pre, pb, bias, biasb))
+        return DG_EINVAL;
+    }
   }
 
   int dev = 0;
@@ -313,6 +350,21 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
   p.ws = pl.ksplit > 1 ? static_cast<float*>(ws) : nullptr;
   p.bias = bias;
   p.act = act;
+  p.epi = {};
+  // nothing that the plain forms lack: they run (the same product and rounding)
+  const bool form3 = rs && (rs->res || rs->pre || act > DG_ACT_GELU);
+  if (form3) {
+    const bool cols8 = N % 8 == 0;
+    p.epi.bias = bias;
+    p.epi.res = rs->res;
+    p.epi.out = static_cast<uint16_t*>(out);
+    p.epi.pre = static_cast<uint16_t*>(rs->pre);
+    p.epi.ldres = rs->ldres;
+    p.epi.res_kind = rs->res ? rs->res_type : dg::kAbsent;
+    p.epi.act = act;
+    p.epi.vec = p.vec_store | (cols8 && ((uintptr_t)rs->pre & 15) == 0 ? 2 : 0) |
+                (((uintptr_t)rs->res & 15) == 0 && (rs->ldres * kind_size(rs->res_type)) % 16 == 0 ? 4 : 0);
+  }
   if (log_enabled())
     std::fprintf(stderr,
                  "dg_gemm_fp8 M=%lld N=%lld K=%lld g=%d layout=%d sa_rows=%d fmt=%d,%d bias=%d act=%d -> kernel %d "
@@ -320,7 +372,8 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
                  (long long)M, (long long)N, (long long)K, gran, layout, sa_rows, fmt_a, fmt_b, bias ? 1 : 0, act, e->id,
                  e->bm, e->bn, e->stages, e->waves, pl.ksplit, (long long)(pl.tiles * pl.ksplit), (long long)need);
   // the streaming entries take every layout themselves
-  t_last_hip = layout == DG_LAYOUT_NT || e->cls == dg::kClassStream
+  t_last_hip = form3 ? dg::launch_residual(e->id, p, static_cast<hipStream_t>(stream))
+               : layout == DG_LAYOUT_NT || e->cls == dg::kClassStream
                    ? e->launch(p, static_cast<hipStream_t>(stream))
                    : dg::launch_layout(e->id, p, static_cast<hipStream_t>(stream));
   return t_last_hip == hipSuccess ? DG_OK : DG_ELAUNCH;
@@ -361,6 +414,182 @@ int quantize(const void* x, int in, int64_t rows, int64_t cols, int gran, int bl
                  (long long)cols, block_rows, gran, fmt, in);
   t_last_hip = block_rows == 1 ? dg::launch_quant_rows(p, static_cast<hipStream_t>(stream))
                                : dg::launch_quant(p, static_cast<hipStream_t>(stream));
+  return t_last_hip == hipSuccess ? DG_OK : DG_ELAUNCH;
+}
+
+// A range of device memory an argument takes; none when p is null.
+struct Range {
+  const void* p;
+  uint64_t n;
+};
+
+// Whether any output overlaps an input or another output, but for the one pair
+// (output `o`, input `i`) that may be the same memory (o < 0: no pair).
+template <int NO, int NI>
+bool clash(const Range (&outs)[NO], const Range (&ins)[NI], int o = -1, int i = -1) {
+  for (int x = 0; x < NO; ++x) {
+    if (!outs[x].p) continue;
+    for (int y = 0; y < NI; ++y)
+      if (ins[y].p && !(x == o && y == i) && overlaps(outs[x].p, outs[x].n, ins[y].p, ins[y].n)) return true;
+    for (int y = 0; y < x; ++y)
+      if (outs[y].p && overlaps(outs[x].p, outs[x].n, outs[y].p, outs[y].n)) return true;
+  }
+  return false;
+}
+
+bool good_dims(int64_t rows, int64_t cols) { return rows > 0 && cols > 0 && rows <= DG_MAX_DIM && cols <= DG_MAX_DIM; }
+bool good_gran(int gran, int64_t cols) { return (gran == 64 || gran == 128 || gran == 256) && cols % gran == 0; }
+bool misaligned(const void* p, uint64_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
+// rows of 16-byte pieces: the base and the row pitch
+bool misaligned_rows(const void* p, int64_t ld, uint64_t esize) { return p && (misaligned(p, 16) || (ld * esize) % 16); }
+
+int rmsnorm_quantize(const void* x, int x_type, int64_t ldx, const void* res, int res_type, int64_t ldres,
+                     const float* w, float eps, int64_t rows, int64_t cols, int gran, int fmt, void* h, void* y,
+                     float* rstd, void* q, float* scales, void* stream) {
+  if (!x || !w || !q || !scales || (!res != !h)) return DG_EINVAL;
+  if (!known_kind(x_type) || (res && !known_kind(res_type))) return DG_EINVAL;
+  if (fmt != DG_FMT_E4M3 && fmt != DG_FMT_E5M2) return DG_EINVAL;
+  if (!good_dims(rows, cols) || !good_gran(gran, cols) || !good_pitch(ldx, cols) || (res && !good_pitch(ldres, cols)))
+    return DG_EINVAL;
+  if (!(eps >= 0.0f) || eps > 1e30f) return DG_EINVAL;
+  const uint64_t xs = kind_size(x_type), rs = res ? kind_size(res_type) : 0;
+  if (misaligned_rows(x, ldx, xs) || misaligned_rows(res, ldres, rs) || misaligned(w, 16) || misaligned(h, 16) ||
+      misaligned(y, 16) || misaligned(q, 8) || misaligned(rstd, 4) || misaligned(scales, 4))
+    return DG_EALIGN;
+  {
+    const uint64_t n = (uint64_t)rows * (uint64_t)cols;
+    const Range outs[] = {{h, n * rs}, {y, n * xs}, {rstd, 4ull * rows}, {q, n}, {scales, 4ull * rows * (cols / gran)}};
+    const Range ins[] = {{x, extent(rows, cols, ldx, xs)}, {res, res ? extent(rows, cols, ldres, rs) : 0}, {w, 4ull * cols}};
+    const bool in_place = h && h == res && ldres == cols;  // a row is read whole before it is written
+    if (clash(outs, ins, in_place ? 0 : -1, 1)) return DG_EINVAL;
+  }
+  const int rc = device_ready();
+  if (rc != DG_OK) return rc;
+  dg::NormArgs p;
+  p.x = x;
+  p.res = res;
+  p.w = w;
+  p.h = h;
+  p.y = y;
+  p.rstd = rstd;
+  p.q = static_cast<uint8_t*>(q);
+  p.scales = scales;
+  p.rows = rows;
+  p.cols = cols;
+  p.ldx = ldx;
+  p.ldres = ldres;
+  p.eps = eps;
+  p.gran = gran;
+  p.fmt = fmt;
+  p.xk = x_type;
+  p.rk = res ? res_type : dg::kAbsent;
+  p.gshift = gran == 64 ? 6 : gran == 128 ? 7 : 8;
+  p.segs = (int)(cols / gran);
+  if (log_enabled())
+    std::fprintf(stderr, "dg_rmsnorm_quantize_fp8 rows=%lld cols=%lld g=%d fmt=%d x=%d res=%d y=%d\n", (long long)rows,
+                 (long long)cols, gran, fmt, x_type, p.rk, y ? 1 : 0);
+  t_last_hip = dg::launch_norm(p, static_cast<hipStream_t>(stream));
+  return t_last_hip == hipSuccess ? DG_OK : DG_ELAUNCH;
+}
+
+int rmsnorm_backward(const void* dy, int dy_type, int64_t lddy, const void* h, int h_type, int64_t ldh,
+                     const float* rstd, const float* w, const void* dh, int64_t lddh, int64_t rows, int64_t cols,
+                     void* dx, float* dw, void* ws, int64_t ws_bytes, void* stream) {
+  if (!dy || !h || !rstd || !w || !dx || !dw) return DG_EINVAL;
+  if (!known_kind(dy_type) || !known_kind(h_type)) return DG_EINVAL;
+  if (!good_dims(rows, cols) || cols % 64 != 0) return DG_EINVAL;
+  if (!good_pitch(lddy, cols) || !good_pitch(ldh, cols) || (dh && !good_pitch(lddh, cols))) return DG_EINVAL;
+  const int64_t need = dg::norm_bwd_workspace(rows, cols);
+  if (ws_bytes < need || (need > 0 && !ws)) return DG_EINVAL;
+  const uint64_t ds = kind_size(dy_type), hs = kind_size(h_type);
+  if (misaligned_rows(dy, lddy, ds) || misaligned_rows(h, ldh, hs) || misaligned_rows(dh, lddh, hs) ||
+      misaligned(w, 16) || misaligned(dx, 16) || misaligned(dw, 4) || misaligned(rstd, 4) || misaligned(ws, 16))
+    return DG_EALIGN;
+  {
+    const Range outs[] = {{dx, hs * rows * cols}, {dw, 4ull * cols}, {need ? ws : nullptr, (uint64_t)need}};
+    const Range ins[] = {{dh, dh ? extent(rows, cols, lddh, hs) : 0},
+                         {dy, extent(rows, cols, lddy, ds)},
+                         {h, extent(rows, cols, ldh, hs)},
+                         {rstd, 4ull * rows},
+                         {w, 4ull * cols}};
+    const bool in_place = dh == dx && lddh == cols;
+    if (clash(outs, ins, in_place ? 0 : -1, 0)) return DG_EINVAL;
+  }
+  const int rc = device_ready();
+  if (rc != DG_OK) return rc;
+  dg::NormBwdArgs p;
+  p.dy = dy;
+  p.h = h;
+  p.rstd = rstd;
+  p.w = w;
+  p.dh = dh;
+  p.dx = dx;
+  p.dw = dw;
+  p.ws = static_cast<float*>(ws);
+  p.rows = rows;
+  p.cols = cols;
+  p.lddy = lddy;
+  p.ldh = ldh;
+  p.lddh = lddh;
+  p.dk = dy_type;
+  p.hk = h_type;
+  if (log_enabled())
+    std::fprintf(stderr, "dg_rmsnorm_backward rows=%lld cols=%lld dy=%d h=%d dh=%d workspace %lld\n", (long long)rows,
+                 (long long)cols, dy_type, h_type, dh ? 1 : 0, (long long)need);
+  t_last_hip = dg::launch_norm_bwd(p, static_cast<hipStream_t>(stream));
+  return t_last_hip == hipSuccess ? DG_OK : DG_ELAUNCH;
+}
+
+int epilogue_backward(const void* dout, int dout_type, int64_t lddout, const void* pre, int64_t ldpre, int act,
+                      int64_t rows, int64_t cols, int gran, int block_rows, int fmt, void* dz, float* dbias, void* q,
+                      float* scales, void* ws, int64_t ws_bytes, void* stream) {
+  if (!dout || !q || !scales) return DG_EINVAL;
+  if (!known_kind(dout_type)) return DG_EINVAL;
+  if (act < DG_ACT_NONE || act > DG_ACT_GELU_TANH || (act != DG_ACT_NONE) != (pre != nullptr)) return DG_EINVAL;
+  if (fmt != DG_FMT_E4M3 && fmt != DG_FMT_E5M2) return DG_EINVAL;
+  if (!good_dims(rows, cols) || !good_gran(gran, cols) || (block_rows != gran && block_rows != 1)) return DG_EINVAL;
+  if (!good_pitch(lddout, cols) || (pre && !good_pitch(ldpre, cols))) return DG_EINVAL;
+  if (((rows + block_rows - 1) / block_rows) * (cols / gran) > 0x7fffffff) return DG_EINVAL;
+  const int64_t need = dbias ? dg::epi_bwd_workspace(rows, cols, gran, block_rows) : 0;
+  if (ws_bytes < need || (need > 0 && !ws)) return DG_EINVAL;
+  const uint64_t ds = kind_size(dout_type);
+  if (misaligned_rows(dout, lddout, ds) || misaligned_rows(pre, ldpre, 2) || misaligned(dz, 16) || misaligned(q, 8) ||
+      misaligned(dbias, 4) || misaligned(scales, 4) || misaligned(ws, 16))
+    return DG_EALIGN;
+  {
+    const uint64_t n = (uint64_t)rows * (uint64_t)cols;
+    const Range outs[] = {{dz, n * ds},
+                          {dbias, 4ull * cols},
+                          {q, n},
+                          {scales, 4ull * ((rows + block_rows - 1) / block_rows) * (cols / gran)},
+                          {need ? ws : nullptr, (uint64_t)need}};
+    const Range ins[] = {{dout, extent(rows, cols, lddout, ds)}, {pre, pre ? extent(rows, cols, ldpre, 2) : 0}};
+    const bool in_place = dz && dz == dout && lddout == cols;
+    if (clash(outs, ins, in_place ? 0 : -1, 0)) return DG_EINVAL;
+  }
+  const int rc = device_ready();
+  if (rc != DG_OK) return rc;
+  dg::EpiBwdArgs p;
+  p.dout = dout;
+  p.pre = static_cast<const uint16_t*>(pre);
+  p.dz = dz;
+  p.dbias = dbias;
+  p.q = static_cast<uint8_t*>(q);
+  p.scales = scales;
+  p.ws = static_cast<float*>(ws);
+  p.rows = rows;
+  p.cols = cols;
+  p.lddout = lddout;
+  p.ldpre = ldpre;
+  p.gran = gran;
+  p.block_rows = block_rows;
+  p.fmt = fmt;
+  p.dk = dout_type;
+  p.act = act;
+  if (log_enabled())
+    std::fprintf(stderr, "dg_epilogue_backward_fp8 rows=%lld cols=%lld block %dx%d fmt=%d act=%d dout=%d workspace %lld\n",
+                 (long long)rows, (long long)cols, block_rows, gran, fmt, act, dout_type, (long long)need);
+  t_last_hip = dg::launch_epi_bwd(p, static_cast<hipStream_t>(stream));
   return t_last_hip == hipSuccess ? DG_OK : DG_ELAUNCH;
 }
 
@@ -498,6 +727,46 @@ int dg_quantize_fp8_blocks_typed(const void* x, int in_type, int64_t rows, int64
 int dg_quantize_fp8_rows_typed(const void* x, int in_type, int64_t rows, int64_t cols, int gran, int fmt, void* q,
                                float* scales, void* stream) {
   return quantize(x, in_type, rows, cols, gran, 1, fmt, q, scales, stream);
+}
+
+int dg_gemm_fp8_residual(const void* a, const void* b, const float* sa, const float* sb, void* out, int64_t M,
+                         int64_t N, int64_t K, int gran, int layout, int sa_rows, int fmt_a, int fmt_b,
+                         const float* bias, int act, const void* res, int res_type, int64_t ldres, void* pre,
+                         void* stream) {
+  const Residual rs{res, res_type, ldres, pre};
+  return gemm(a, b, sa, sb, out, M, N, K, gran, layout, sa_rows, fmt_a, fmt_b, bias, act, stream, false, nullptr, 0,
+              false, &rs);
+}
+
+int dg_rmsnorm_quantize_fp8(const void* x, int x_type, int64_t ldx, const void* res, int res_type, int64_t ldres,
+                            const float* w, float eps, int64_t rows, int64_t cols, int gran, int fmt, void* h, void* y,
+                            float* rstd, void* q, float* scales, void* stream) {
+  return rmsnorm_quantize(x, x_type, ldx, res, res_type, ldres, w, eps, rows, cols, gran, fmt, h, y, rstd, q, scales,
+                          stream);
+}
+
+int64_t dg_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+  return good_dims(rows, cols) && cols % 64 == 0 ? dg::norm_bwd_workspace(rows, cols) : (int64_t)DG_EINVAL;
+}
+
+int dg_rmsnorm_backward(const void* dy, int dy_type, int64_t lddy, const void* h, int h_type, int64_t ldh,
+                        const float* rstd, const float* w, const void* dh, int64_t lddh, int64_t rows, int64_t cols,
+                        void* dx, float* dw, void* workspace, int64_t workspace_bytes, void* stream) {
+  return rmsnorm_backward(dy, dy_type, lddy, h, h_type, ldh, rstd, w, dh, lddh, rows, cols, dx, dw, workspace,
+                          workspace_bytes, stream);
+}
+
+int64_t dg_epilogue_backward_workspace(int64_t rows, int64_t cols, int gran, int block_rows) {
+  return good_dims(rows, cols) && good_gran(gran, cols) && (block_rows == gran || block_rows == 1)
+             ? dg::epi_bwd_workspace(rows, cols, gran, block_rows)
+             : (int64_t)DG_EINVAL;
+}
+
+int dg_epilogue_backward_fp8(const void* dout, int dout_type, int64_t lddout, const void* pre, int64_t ldpre, int act,
+                             int64_t rows, int64_t cols, int gran, int block_rows, int fmt, void* dz, float* dbias,
+                             void* q, float* scales, void* workspace, int64_t workspace_bytes, void* stream) {
+  return epilogue_backward(dout, dout_type, lddout, pre, ldpre, act, rows, cols, gran, block_rows, fmt, dz, dbias, q,
+                           scales, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

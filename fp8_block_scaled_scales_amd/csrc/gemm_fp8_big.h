@@ -119,7 +119,7 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
                                                       const float* __restrict__ sa, const float* __restrict__ sb,
                                                       uint16_t* __restrict__ out, int M, int N, int K, int tiles_m,
                                                       int tiles_n, int vec_store, int sshift,
-                                                      const float* __restrict__ bias, int relu) {
+                                                      const float* __restrict__ bias, int relu, const EpiArgs epi) {
   static_assert(G == 64 || G == 128, "granularity");
   constexpr int WN = NW / WM;
   constexpr int WTM = BM / WM, WTN = BN / WN;
@@ -212,13 +212,15 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
   // copies: the step waits cover it, and no output store is in flight when
   // the epilogue reads it. The plain form (EPI 0) loads and holds nothing.
   constexpr int NBJ = G == 128 ? WTN / 16 : WTN / 32;
-  const bool hb = EPI != 0 && bias != nullptr;
+  const bool hb = (EPI == 1 || EPI == 2) && bias != nullptr;
   float bj[NBJ];
 #pragma unroll
   for (int j = 0; j < NBJ; ++j) {
     const int col = wc0 + (G == 128 ? j * 16 + (lane & 15) : j * 32 + (lane & 31));
     bj[j] = hb && col < N ? bias[col] : 0.0f;
   }
+  float b8[8];  // form 3: the columns this thread stores
+  if constexpr (EPI == 3) load_bias<8>(epi, n0 + (threadIdx.x % (BN / 8)) * 8, N, b8);
 
   issue_step(0);
 
@@ -381,9 +383,41 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
     DG_STEP_SYNC_WG();
   }
   DG_WAIT_VMCNT(0);
+  if constexpr (EPI == 3) {
+    // 32 rows of every wave row at a time, so that all waves write and all
+    // threads store in every pass. The pitch puts rows four apart 16 banks
+    // apart, where the 16x16 layout's lane groups write them.
+    constexpr int GR = 32, LDF = BN + 4;
+    static_assert(WM * GR * LDF * 4 <= 2 * SLOT, "an epilogue pass must fit in the ring");
+    float* const cf = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int pass = 0; pass < WTM / GR; ++pass) {
+      __syncthreads();
+      if constexpr (G == 128) {
+        const int r16 = lane & 15, q = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < WTN / 16; ++j)
+#pragma unroll
+          for (int i = 0; i < GR / 16; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              cf[(wm * GR + i * 16 + 4 * q + v) * LDF + wn * WTN + j * 16 + r16] = acc.t[pass * (GR / 16) + i][j][v];
+      } else {
+        const int r32 = lane & 31, h2 = lane >> 5;
+#pragma unroll
+        for (int j = 0; j < WTN / 32; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            cf[(wm * GR + 8 * (v >> 2) + 4 * h2 + (v & 3)) * LDF + wn * WTN + j * 32 + r32] = acc.t[pass][j][v];
+      }
+      __syncthreads();
+      residual_pass<BN, LDF, NT, WM, WTM, GR>(epi, cf, m0, n0, pass * GR, M, N, b8);
+    }
+    return;
+  }
   // Bias and activation in place, by all eight waves at once (the passes
   // below keep half of them idle).
-  if constexpr (EPI != 0) {
+  if constexpr (EPI == 1 || EPI == 2) {
     if constexpr (G == 128) {
 #pragma unroll
       for (int j = 0; j < WTN / 16; ++j)
@@ -457,7 +491,7 @@ hipError_t launch_fa(const GemmArgs& p, hipStream_t stream) {
   const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
   hipLaunchKernelGGL((gemm_fp8_nt_big<G, BN, WM, 4, FMT, EPI, ROWA, LAYOUT>), dim3(tiles_m * tiles_n), dim3(NT), 0, stream, p.a,
                      p.b, p.sa, p.sb, p.out, (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.vec_store, p.sshift,
-                     p.bias, p.act == 1 ? 1 : 0);
+                     p.bias, p.act == 1 ? 1 : 0, p.epi);
   return hipGetLastError();
 }
 
@@ -486,14 +520,22 @@ hipError_t launch_fmt(const GemmArgs& p, hipStream_t stream) {
   }
 }
 
-template <int G, int BN, int WM, int LAYOUT, int RS>
+// RES: the form with a residual (3) alone; else the forms without, by bias
+// and activation.
+template <int G, int BN, int WM, int FMT, int LAYOUT, int RS, bool RES>
+hipError_t launch_form(const GemmArgs& p, hipStream_t stream) {
+  if constexpr (RES) return launch_sa<G, BN, WM, FMT, 3, LAYOUT, RS>(p, stream);
+  else return launch_fmt<G, BN, WM, FMT, LAYOUT, RS>(p, stream);
+}
+
+template <int G, int BN, int WM, int LAYOUT, int RS, bool RES = false>
 hipError_t launch_l(const GemmArgs& p, hipStream_t stream) {
   if (p.ksplit != 1 || p.sshift < 0 || p.sshift > 1) return hipErrorInvalidValue;
   switch (p.fmt) {
-    case 0: return launch_fmt<G, BN, WM, 0, LAYOUT, RS>(p, stream);
-    case 1: return launch_fmt<G, BN, WM, 1, LAYOUT, RS>(p, stream);
-    case 2: return launch_fmt<G, BN, WM, 2, LAYOUT, RS>(p, stream);
-    case 3: return launch_fmt<G, BN, WM, 3, LAYOUT, RS>(p, stream);
+    case 0: return launch_form<G, BN, WM, 0, LAYOUT, RS, RES>(p, stream);
+    case 1: return launch_form<G, BN, WM, 1, LAYOUT, RS, RES>(p, stream);
+    case 2: return launch_form<G, BN, WM, 2, LAYOUT, RS, RES>(p, stream);
+    case 3: return launch_form<G, BN, WM, 3, LAYOUT, RS, RES>(p, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -512,6 +554,18 @@ hipError_t launch_layout(const GemmArgs& p, hipStream_t stream) {
     case 1: return launch_l<G, BN, WM, 1, RS>(p, stream);
     case 2: return launch_l<G, BN, WM, 2, RS>(p, stream);
     case 3: return launch_l<G, BN, WM, 3, RS>(p, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// The form with a residual, every layout.
+template <int G, int BN, int WM, int RS>
+hipError_t launch_res(const GemmArgs& p, hipStream_t stream) {
+  switch (p.layout) {
+    case 0: return launch_l<G, BN, WM, 0, RS, true>(p, stream);
+    case 1: return launch_l<G, BN, WM, 1, RS, true>(p, stream);
+    case 2: return launch_l<G, BN, WM, 2, RS, true>(p, stream);
+    case 3: return launch_l<G, BN, WM, 3, RS, true>(p, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gemm_epilogue.h"
+
 namespace dg {
 
 struct GemmArgs {
@@ -22,7 +24,8 @@ struct GemmArgs {
   int ksplit;     // workgroups per output tile along K (1 = no split)
   float* ws;      // split-K partial tiles, tiles * ksplit * bm * bn floats (ksplit > 1; caller's workspace)
   const float* bias;   // FP32 [N] added before the activation, or null
-  int act;             // epilogue activation: 0 none, 1 ReLU, 2 GELU
+  int act;             // epilogue activation: 0 none, 1 ReLU, 2 GELU; with form 3 also 3 SiLU, 4 GELU (tanh form)
+  EpiArgs epi;         // form 3 (launch_residual): residual, pre-activation and all of the above again
 };
 
 typedef hipError_t (*Launcher)(const GemmArgs&, hipStream_t);
@@ -66,6 +69,12 @@ hipError_t launch_layout(int id, const GemmArgs& p, hipStream_t stream);
 hipError_t launch_big_layout(int id, const GemmArgs& p, hipStream_t stream);
 hipError_t launch_layout_rowa(int id, const GemmArgs& p, hipStream_t stream);
 hipError_t launch_big_layout_rowa(int id, const GemmArgs& p, hipStream_t stream);
+
+// The epilogue with a residual or a kept pre-activation (GemmArgs::epi), every
+// layout and factor form of table entry `id`.
+hipError_t launch_residual(int id, const GemmArgs& p, hipStream_t stream);
+hipError_t launch_residual_big(int id, const GemmArgs& p, hipStream_t stream);
+hipError_t launch_residual_big_rowa(int id, const GemmArgs& p, hipStream_t stream);
 
 extern KernelEntry kTable[];
 extern const int kTableSize;

@@ -66,7 +66,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
     const uint8_t* __restrict__ a, const uint8_t* __restrict__ b, const float* __restrict__ sa,
     const float* __restrict__ sb, uint16_t* __restrict__ out, int M, int N, int K, int tiles_m,
     int tiles_n, int vec_store, int ksplit, float* __restrict__ ws, int sshift, const float* __restrict__ bias,
-    int relu) {
+    int relu, const EpiArgs epi) {
   constexpr int NWAVES = WM * WN;
   constexpr int NT = 64 * NWAVES;
   constexpr int WTM = BM / WM, WTN = BN / WN;  // wave tile
@@ -147,13 +147,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
   // The epilogue's bias for this lane's columns, loaded before the first
   // copies: the step waits cover it, and no output store is in flight when
   // the epilogue reads it.
-  const bool hb = EPI != 0 && bias != nullptr;
+  const bool hb = (EPI == 1 || EPI == 2) && bias != nullptr;
   float bcol[TN];
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     const int col = n0 + wn * WTN + j * 32 + (lane & 31);
     bcol[j] = hb && col < N ? bias[col] : 0.0f;
   }
+  float b8[8];  // form 3: the columns this thread stores
+  if constexpr (EPI == 3) load_bias<8>(epi, n0 + (threadIdx.x % (BN / 8)) * 8, N, b8);
 
   // Prologue: fill STAGES-1 ring slots.
 #pragma unroll
@@ -264,6 +266,25 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
     return;
   }
 
+  if constexpr (EPI == 3) {
+    // one 32-row sub-tile of every wave row at a time
+    constexpr int LDF = BN + 4;
+    static_assert(WM * 32 * LDF * 4 <= STAGES * STAGE_BYTES, "an epilogue pass must fit in the ring");
+    float* const cf = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          cf[(wm * 32 + (v >> 2) * 8 + half * 4 + (v & 3)) * LDF + wn * WTN + j * 32 + (lane & 31)] = acc[i][j][v];
+      __syncthreads();
+      residual_pass<BN, LDF, NT, WM, WTM, 32>(epi, cf, m0, n0, i * 32, M, N, b8);
+    }
+    return;
+  }
+
   // Epilogue: BF16 tile through LDS, then 16-byte row-contiguous stores.
   __syncthreads();
   uint16_t* cs = reinterpret_cast<uint16_t*>(smem);
@@ -342,13 +363,15 @@ static hipError_t launch_tiled_fa(const GemmArgs& p, hipStream_t stream) {
   hipLaunchKernelGGL((gemm_fp8_nt_tiled<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, FMT, EPI, ROWA, LAYOUT>),
                      dim3(tiles_m * tiles_n * p.ksplit), dim3(64 * WM * WN), 0, stream, p.a, p.b, p.sa, p.sb, p.out,
                      (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.vec_store, p.ksplit, p.ws, p.sshift, p.bias,
-                     p.act == 1 ? 1 : 0);
+                     p.act == 1 ? 1 : 0, p.epi);
   hipError_t err = hipGetLastError();
-  if (SPLIT && p.ksplit > 1 && err == hipSuccess) {
-    hipLaunchKernelGGL((splitk_reduce<BM, BN, EPI>), dim3(tiles_m * tiles_n * (BM * BN / 4 / 256)), dim3(256), 0,
-                       stream, p.ws, p.out, (int)p.M, (int)p.N, tiles_n, p.ksplit, p.vec_store, p.bias,
-                       p.act == 1 ? 1 : 0);
-    err = hipGetLastError();
+  if constexpr (SPLIT && EPI != 3) {  // the form with a residual is planned without a split
+    if (p.ksplit > 1 && err == hipSuccess) {
+      hipLaunchKernelGGL((splitk_reduce<BM, BN, EPI>), dim3(tiles_m * tiles_n * (BM * BN / 4 / 256)), dim3(256), 0,
+                         stream, p.ws, p.out, (int)p.M, (int)p.N, tiles_n, p.ksplit, p.vec_store, p.bias,
+                         p.act == 1 ? 1 : 0);
+      err = hipGetLastError();
+    }
   }
   return err;
 }
@@ -381,14 +404,24 @@ static hipError_t launch_tiled_fmt(const GemmArgs& p, hipStream_t stream) {
   }
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int G, int GROUP_M, bool SPLIT, int LAYOUT, int RS>
+// RES: the form with a residual (3) alone; else the forms without, by bias
+// and activation.
+template <int BM, int BN, int WM, int WN, int STAGES, int G, int GROUP_M, bool SPLIT, int FMT, int LAYOUT, int RS,
+          bool RES>
+static hipError_t launch_tiled_form(const GemmArgs& p, hipStream_t stream) {
+  if constexpr (RES) return launch_tiled_sa<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, FMT, 3, LAYOUT, RS>(p, stream);
+  else return launch_tiled_fmt<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, FMT, LAYOUT, RS>(p, stream);
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, int G, int GROUP_M, bool SPLIT, int LAYOUT, int RS,
+          bool RES = false>
 static hipError_t launch_tiled_l(const GemmArgs& p, hipStream_t stream) {
-  if ((!SPLIT && p.ksplit != 1) || p.sshift < 0 || p.sshift > 1) return hipErrorInvalidValue;
+  if (((!SPLIT || RES) && p.ksplit != 1) || p.sshift < 0 || p.sshift > 1) return hipErrorInvalidValue;
   switch (p.fmt) {
-    case 0: return launch_tiled_fmt<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 0, LAYOUT, RS>(p, stream);
-    case 1: return launch_tiled_fmt<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 1, LAYOUT, RS>(p, stream);
-    case 2: return launch_tiled_fmt<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 2, LAYOUT, RS>(p, stream);
-    case 3: return launch_tiled_fmt<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 3, LAYOUT, RS>(p, stream);
+    case 0: return launch_tiled_form<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 0, LAYOUT, RS, RES>(p, stream);
+    case 1: return launch_tiled_form<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 1, LAYOUT, RS, RES>(p, stream);
+    case 2: return launch_tiled_form<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 2, LAYOUT, RS, RES>(p, stream);
+    case 3: return launch_tiled_form<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 3, LAYOUT, RS, RES>(p, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -408,6 +441,18 @@ static hipError_t launch_tiled_layout(const GemmArgs& p, hipStream_t stream) {
     case 1: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 1, RS>(p, stream);
     case 2: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 2, RS>(p, stream);
     case 3: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 3, RS>(p, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// The form with a residual, every layout and factor form.
+template <int BM, int BN, int WM, int WN, int STAGES, int G, int GROUP_M, bool SPLIT>
+static hipError_t launch_tiled_res(const GemmArgs& p, hipStream_t stream) {
+  switch (p.layout) {
+    case 0: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 0, 0, true>(p, stream);
+    case 1: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 1, 0, true>(p, stream);
+    case 2: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 2, 0, true>(p, stream);
+    case 3: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 3, 0, true>(p, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -31,153 +31,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "quant_common.h"
 #include "quant_fp8.h"
 
 namespace dg {
-
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef unsigned v4u __attribute__((ext_vector_type(4)));
-typedef int v2i __attribute__((ext_vector_type(2)));
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-
-// Input element kinds: 0 FP32, 1 BF16, 2 FP16 (the library's DG_IN_* codes).
-template <int IN>
-struct InKind {
-  static constexpr int kBytes = IN == 0 ? 4 : 2;  // bytes per element
-  static constexpr int kPerLoad = 16 / kBytes;     // elements per 16-byte load
-  static constexpr int kQuads = kPerLoad / 4;      // groups of four per load
-};
-
-// Elements 4*H .. 4*H+3 of a 16-byte load, as FP32 (exact for every kind).
-// A 32-bit word holds two 16-bit elements, the first in its low half. BF16 is
-// the high half of an FP32 pattern; FP16 converts exactly.
-template <int IN, int H>
-__device__ __forceinline__ v4f widen(v4u w) {
-  if constexpr (IN == 0) {
-    return __builtin_bit_cast(v4f, w);
-  } else {
-    const unsigned a = H ? w.z : w.x, b = H ? w.w : w.y;
-    if constexpr (IN == 1) {
-      return (v4f){__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
-                   __uint_as_float(b & 0xFFFF0000u)};
-    } else {
-      const v2h ha = __builtin_bit_cast(v2h, a), hb = __builtin_bit_cast(v2h, b);
-      return (v4f){(float)ha.x, (float)ha.y, (float)hb.x, (float)hb.y};
-    }
-  }
-}
-
-__device__ __forceinline__ float amax4(v4f v) {
-  return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-}
-
-typedef unsigned short v2u16 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ v2u16 abs_bits2(unsigned w) { return __builtin_bit_cast(v2u16, w & 0x7FFF7FFFu); }
-
-// max |x| over the elements of one 16-byte load. For 16-bit input the max is
-// taken on the bit patterns: with the sign bit cleared, the patterns of
-// finite BF16 or FP16 values order as the magnitudes do, so a packed 16-bit
-// integer max finds the largest, which is then widened once. Nothing widened
-// here stays live until the encode pass, which widens its own copies.
-template <int IN>
-__device__ __forceinline__ float amax_load(v4u w) {
-  if constexpr (IN == 0) {
-    return amax4(widen<IN, 0>(w));
-  } else {
-    const v2u16 m = __builtin_elementwise_max(__builtin_elementwise_max(abs_bits2(w.x), abs_bits2(w.y)),
-                                              __builtin_elementwise_max(abs_bits2(w.z), abs_bits2(w.w)));
-    const unsigned top = m.x > m.y ? m.x : m.y;
-    if constexpr (IN == 1) return __uint_as_float(top << 16);
-    else return (float)__builtin_bit_cast(_Float16, (unsigned short)top);
-  }
-}
-
-// Division by a block's scale s, rounded as the correctly rounded FP32 divide
-// rounds it, without a divide per element. inv = RN(1/s) is computed once per
-// block (a correctly rounded divide); per element q0 = RN(x * inv) lies within
-// 1.5 ulp of x/s, one correction q1 = RN(q0 + RN(x - q0*s) * inv) (the
-// remainder exact under the FMA) brings it within one ulp, and a second
-// correction then gives RN(x/s) by Markstein's theorem on FMA-based division
-// (P. Markstein, "IA-64 and Elementary Functions", 2000; also the chapter on
-// division with an FMA in the Handbook of Floating-Point Arithmetic): with a
-// correctly rounded reciprocal and a quotient within one ulp, the corrected
-// quotient is the correctly rounded one. The theorem asks that nothing
-// overflows or underflows: s and 1/s normal (the caller's uniform test,
-// recip_ok; blocks outside it divide per element) and x/s at most the
-// format's largest value. A quotient in FP32's subnormal range may come out
-// wrong in its last bits, but every such value is far below half the smallest
-// FP8 subnormal and encodes to a signed zero either way; the sign is x's (an
-// input -0 gives -0, where the corrections alone would give +0).
-// A block's factor: amax / fmax (correctly rounded), or 1.0 where that is
-// zero: an all-zero block, or one whose amax is so small that the quotient
-// underflows (no factor of zero to divide by; 1.0 encodes its values, all
-// below fmax * 2^-150, under 2^-134, as zeros).
-__device__ __forceinline__ float block_scale(float amax, float fmax) {
-  const float s = amax / fmax;
-  return s > 0.0f ? s : 1.0f;
-}
-
-__device__ __forceinline__ bool recip_ok(float s) { return s >= 0x1p-120f && s <= 0x1p120f; }
-
-__device__ __forceinline__ float div_by_scale(float x, float s, float inv) {
-  float q = x * inv;
-  q = __builtin_fmaf(__builtin_fmaf(-q, s, x), inv, q);
-  q = __builtin_fmaf(__builtin_fmaf(-q, s, x), inv, q);
-  return __builtin_copysignf(q, x);
-}
-
-// One DPP move of v across the wave (row_mask, bank_mask all on; every
-// source lane exists for the patterns used here).
-template <int CTRL>
-__device__ __forceinline__ float dpp_f(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
-
-// Max over each aligned group of L lanes (L = 8, 16, 32 or 64), in every lane
-// of the group: within quads by two swaps (DPP quad_perm [1,0,3,2],
-// [2,3,0,1]), then each lane against its mirror in the 8-lane half row, which
-// leaves the half row's max in every lane, and in the 16-lane row (DPP
-// row_half_mirror, row_mirror); beyond 16 lanes, cross-lane shuffles. max is
-// exact and order-free.
-template <int L>
-__device__ __forceinline__ float group_max(float m) {
-  static_assert(L == 8 || L == 16 || L == 32 || L == 64, "group");
-  m = fmaxf(m, dpp_f<0xB1>(m));
-  m = fmaxf(m, dpp_f<0x4E>(m));
-  m = fmaxf(m, dpp_f<0x141>(m));
-  if constexpr (L >= 16) m = fmaxf(m, dpp_f<0x140>(m));
-  if constexpr (L >= 32) m = fmaxf(m, __shfl_xor(m, 16, 64));
-  if constexpr (L >= 64) m = fmaxf(m, __shfl_xor(m, 32, 64));
-  return m;
-}
-
-// Two FP8 codes of (x0, x1) packed into the low (HI = false) or high half of
-// `old`: FMT 0 E4M3FN, 1 E5M2 (hardware round-to-nearest-even).
-template <int FMT, bool HI>
-__device__ __forceinline__ int cvt2(float x0, float x1, int old) {
-  if constexpr (FMT == 1) return __builtin_amdgcn_cvt_pk_bf8_f32(x0, x1, old, HI);
-  else return __builtin_amdgcn_cvt_pk_fp8_f32(x0, x1, old, HI);
-}
-
-// Four codes of v / s in one 32-bit word (bytes in element order). FAST (s
-// and 1/s normal): |v / s| rounds to at most fmax, since s carries a relative
-// error of at most 2^-24. Otherwise s is subnormal or tiny, its own rounding
-// can be coarse enough that |v / s| passes fmax, and the quotient saturates
-// to +-fmax as FP8's round-to-nearest with saturation takes it (the
-// conversion instruction alone does not saturate).
-template <int FMT, bool FAST>
-__device__ __forceinline__ int encode4(v4f v, float s, float inv) {
-  if constexpr (FAST) {
-    const int lo = cvt2<FMT, false>(div_by_scale(v.x, s, inv), div_by_scale(v.y, s, inv), 0);
-    return cvt2<FMT, true>(div_by_scale(v.z, s, inv), div_by_scale(v.w, s, inv), lo);
-  } else {
-    constexpr float FMAX = FMT == 1 ? 57344.0f : 448.0f;
-    auto sat = [](float y) { return fminf(fmaxf(y, -FMAX), FMAX); };
-    const int lo = cvt2<FMT, false>(sat(v.x / s), sat(v.y / s), 0);
-    return cvt2<FMT, true>(sat(v.z / s), sat(v.w / s), lo);
-  }
-}
 
 // The codes of one 16-byte load's elements, divided by s, stored at q (4 or
 // 8 bytes: one code per element, in element order).

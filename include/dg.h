@@ -58,11 +58,13 @@ extern "C" {
 #define DG_ELAUNCH (-4)      /* a HIP call failed (not recoverable); dg_strerror() gives its text */
 #define DG_ESCRATCH (-5)     /* dg_gemm_fp8_noalloc: the plan needs more than its fixed scratch; nothing launched */
 
-/* Version of this header and library: 2.1.0 (2.0.0: dg_tile_info gained
+/* Version of this header and library: 2.2.0 (2.0.0: dg_tile_info gained
  * workspace_bytes; dg_gemm_fp8_ws and dg_query_tile_ws were added; no call
  * but dg_gemm_fp8_ws splits K over workgroups. 2.1.0: the quantisers take
- * BF16 and FP16 input through the _typed calls). */
-#define DG_VERSION 210
+ * BF16 and FP16 input through the _typed calls. 2.2.0: the RMS norm with FP8
+ * output and its backward pass, the product with a residual in its epilogue,
+ * and the gradient through that epilogue). */
+#define DG_VERSION 220
 
 /* Largest accepted dimension, 2^24 - 256: a 256-row tile of K bytes per row
  * (256 * K) then stays below 2^32 bytes, the reach of a buffer descriptor,
@@ -367,6 +369,135 @@ int dg_quantize_fp8_blocks_typed(const void* x, int in_type, int64_t rows, int64
                                  float* scales, void* stream);
 int dg_quantize_fp8_rows_typed(const void* x, int in_type, int64_t rows, int64_t cols, int gran, int fmt, void* q,
                                float* scales, void* stream);
+
+/* ---- The operators around the product in a transformer layer -------------
+ *
+ * norm -> product -> ... -> product + residual, and the way back. Element types
+ * are DG_IN_F32, DG_IN_BF16 or DG_IN_F16 where a *_type is given. An input
+ * matrix with a row pitch (ld*, in elements, at least its columns and at most
+ * DG_MAX_DIM) may be a slice of a wider one; outputs are row-major without
+ * gaps. Inputs must be finite, as for the quantisers. Outputs overlap no other
+ * argument (DG_EINVAL) except where a call says that one may be an input
+ * itself. Sums are FP32 in a fixed order, with no atomics: a call repeated on
+ * the same arguments gives the same bits.
+ */
+
+/* Activations of the calls below, beside DG_ACT_NONE, _RELU and _GELU. */
+#define DG_ACT_SILU 3      /* y / (1 + exp(-y)) */
+#define DG_ACT_GELU_TANH 4 /* 0.5 y (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))) */
+
+/*
+ * dg_gemm_fp8_residual - the product with bias, activation and residual in its
+ * epilogue, and the pre-activation kept for a backward pass:
+ *
+ *   z = C[i,j] + bias[j];  pre[i,j] = bf16(z);  out[i,j] = bf16(act(z) + res[i,j])
+ *
+ * in FP32, each output rounded once.
+ *
+ *   a, b, sa, sb, out, M, N, K, gran, layout, sa_rows, fmt_a, fmt_b, bias
+ *        as dg_gemm_fp8_ws without a workspace (the same tile choice).
+ *   act  any of the five DG_ACT_* codes.
+ *   res  [M][N] of res_type, row pitch ldres, aligned to its element, or NULL
+ *        (res_type and ldres are then not read). It may be out itself (BF16,
+ *        ldres = N): the stream is updated in place.
+ *   pre  BF16 [M][N] out, 2-byte aligned, or NULL.
+ *
+ * Without res and pre and with one of the three activations of
+ * dg_gemm_fp8_layout the result is that call's, bit for bit (with sa_rows = 1
+ * dg_gemm_fp8_ws's). Accesses to out, pre and res are 16 bytes wide where
+ * their bases and pitches allow it. Status codes as dg_gemm_fp8_layout.
+ */
+int dg_gemm_fp8_residual(const void* a, const void* b, const float* sa, const float* sb, void* out, int64_t M,
+                         int64_t N, int64_t K, int gran, int layout, int sa_rows, int fmt_a, int fmt_b,
+                         const float* bias, int act, const void* res, int res_type, int64_t ldres, void* pre,
+                         void* stream);
+
+/*
+ * dg_rmsnorm_quantize_fp8 - the residual's addition, the root-mean-square norm
+ * and the 1 x gran quantisation of its output in one pass:
+ *
+ *   h    = x + res rounded to res_type (no residual: h = x)
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps)
+ *   y    = h * rstd * w
+ *   scales, q: dg_quantize_fp8_rows's rule on the FP32 y
+ *
+ *   x      [rows][cols] of x_type, row pitch ldx; 16-byte aligned base and pitch.
+ *   res    the same of res_type, or NULL with h NULL.
+ *   w      FP32 [cols], 16-byte aligned.
+ *   eps    >= 0. (A row of zeros with eps = 0 has no norm: its codes are NaN.)
+ *   gran   64, 128 or 256, dividing cols.  fmt  DG_FMT_E4M3 or DG_FMT_E5M2.
+ *   h      out, [rows][cols] of res_type, 16-byte aligned; may be res itself
+ *          (ldres = cols).
+ *   y      out, [rows][cols] of x_type, 16-byte aligned, or NULL: kept by a
+ *          forward pass that trains (the weight gradient's operand).
+ *   rstd   out, FP32 [rows], or NULL.
+ *   q      FP8 codes out, [rows][cols], 8-byte aligned.
+ *   scales FP32 out, [rows][cols/gran]: what dg_gemm_fp8_nt_ex takes with
+ *          sa_rows = 1.
+ *
+ * Squares are summed in FP32: a row whose sum of squares passes 3.4e38
+ * overflows. Returns DG_OK, DG_EINVAL, DG_EALIGN, DG_EUNSUPPORTED or
+ * DG_ELAUNCH.
+ */
+int dg_rmsnorm_quantize_fp8(const void* x, int x_type, int64_t ldx, const void* res, int res_type, int64_t ldres,
+                            const float* w, float eps, int64_t rows, int64_t cols, int gran, int fmt, void* h, void* y,
+                            float* rstd, void* q, float* scales, void* stream);
+
+/*
+ * dg_rmsnorm_backward - the gradient of that norm, with n = h * rstd and
+ * u = dy * w:
+ *
+ *   dx = rstd * (u - n * mean over the row of u * n) + dh
+ *   dw = sum over the rows of dy * n
+ *
+ *   dy     gradient of y, [rows][cols] of dy_type, row pitch lddy.
+ *   h      the stream that was normed, of h_type, row pitch ldh.
+ *   rstd, w  as the forward pass wrote and read them.
+ *   dh     gradient that reaches h past the norm, of h_type, row pitch lddh, or
+ *          NULL (none).
+ *   dx     out, [rows][cols] of h_type, 16-byte aligned: the gradient of x and
+ *          of the residual alike; may be dh itself (lddh = cols).
+ *   dw     out, FP32 [cols].
+ *   cols   a multiple of 64. dy, h, dh: 16-byte aligned bases and pitches.
+ *   workspace  device memory of at least dg_rmsnorm_backward_workspace bytes,
+ *          16-byte aligned (NULL where that is 0); scratch, as dg_gemm_fp8_ws's:
+ *          calls that may overlap in time need distinct ones.
+ */
+int dg_rmsnorm_backward(const void* dy, int dy_type, int64_t lddy, const void* h, int h_type, int64_t ldh,
+                        const float* rstd, const float* w, const void* dh, int64_t lddh, int64_t rows, int64_t cols,
+                        void* dx, float* dw, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of that call (DG_EINVAL for sizes it would reject). */
+int64_t dg_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * dg_epilogue_backward_fp8 - the gradient through an epilogue
+ * out = act(z) [+ residual], z = C + bias, quantised for the products that
+ * follow (the residual's gradient is dout itself):
+ *
+ *   dz     = dout * act'(pre)      (DG_ACT_NONE: dout, with pre NULL)
+ *   scales, q: the quantisers' rule on the FP32 dz, with gran x gran blocks
+ *          (block_rows = gran) or one factor per row and segment (1)
+ *   dbias  = sum over the rows of dz
+ *
+ *   dout   [rows][cols] of dout_type, row pitch lddout; 16-byte aligned base
+ *          and pitch.  pre  BF16, row pitch ldpre, the same.
+ *   dz     out, [rows][cols] of dout_type, 16-byte aligned, or NULL; may be
+ *          dout itself (lddout = cols).
+ *   dbias  out, FP32 [cols], or NULL.
+ *   q      FP8 codes out, [rows][cols], 8-byte aligned.
+ *   scales FP32 out, [ceil(rows/block_rows)][cols/gran].
+ *   workspace  at least dg_epilogue_backward_workspace bytes with dbias (NULL
+ *          where that is 0, and without dbias), 16-byte aligned; as above.
+ *
+ * ReLU's derivative at 0 is 0.
+ */
+int dg_epilogue_backward_fp8(const void* dout, int dout_type, int64_t lddout, const void* pre, int64_t ldpre, int act,
+                             int64_t rows, int64_t cols, int gran, int block_rows, int fmt, void* dz, float* dbias,
+                             void* q, float* scales, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of that call with dbias (DG_EINVAL for sizes it would reject). */
+int64_t dg_epilogue_backward_workspace(int64_t rows, int64_t cols, int gran, int block_rows);
 
 /* Text for a status code (for DG_ELAUNCH: the last HIP error on this
  * thread), so a caller can log which class of failure (the pitfalls article
