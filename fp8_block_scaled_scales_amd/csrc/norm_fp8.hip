@@ -24,6 +24,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "layer_ops.h"
 #include "quant_common.h"
 
@@ -191,51 +193,212 @@ hipError_t launch_norm_x(const NormArgs& p, hipStream_t stream) {
 
 // ---- backward -----------------------------------------------------------------
 
-// dx of one row per RT threads.
+// u * n and dy * n of eight elements: their contributions to the row's sum and
+// to the columns' sums.
+template <int DK, int HK>
+__device__ __forceinline__ float row_part8(const Raw8<DK>& dy, const Raw8<HK>& h, const float (&w)[8], float rstd) {
+  float g[8], n[8], s = 0.0f;
+  widen8(dy, g);
+  widen8(h, n);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s = __builtin_fmaf(g[k] * w[k], n[k] * rstd, s);
+  return s;
+}
+
+// dx of eight elements from the row's mean of u * n.
+template <int DK, int HK>
+__device__ __forceinline__ void store_dx8(const NormBwdArgs& p, const Raw8<DK>& dy, const Raw8<HK>& h, const Raw8<HK>& dh,
+                                          const float (&w)[8], float rstd, float mean, int64_t e) {
+  float g[8], n[8], d[8];
+  widen8(dy, g);
+  widen8(h, n);
+  widen8(dh, d);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) d[k] = __builtin_fmaf(rstd, g[k] * w[k] - n[k] * rstd * mean, d[k]);
+  store8<HK>(p.dx, e, round8<HK>(d));
+}
+
+template <int HK>
+__device__ __forceinline__ Raw8<HK> load_dh8(const NormBwdArgs& p, int64_t row, int c) {
+  return p.dh ? load8<HK>(p.dh, row * p.lddh + c) : Raw8<HK>{};
+}
+
+// Few rows, one launch and no workspace: the first `col_wgs` workgroups add
+// dy * n over all rows, 64 columns each (eight lanes of eight columns, their
+// sums over the threads' rows added through LDS in a fixed order); the others
+// take a row per RT threads. dy and h are read twice, from L2 the second time.
 template <int DK, int HK, int RT, int C>
-__global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_rows(const NormBwdArgs p) {
-  constexpr int ROWS = RT < 256 ? 256 / RT : 1;
-  __shared__ float red[RT / 64];
+__global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_few(const NormBwdArgs p, int col_wgs) {
+  constexpr int NT = RT < 256 ? 256 : RT, ROWS = NT / RT, RL = NT / 8;
+  __shared__ float red[RL][64];
+  if ((int)blockIdx.x < col_wgs) {
+    const int cl = threadIdx.x % 8, rl = threadIdx.x / 8;
+    const int c = blockIdx.x * 64 + cl * 8;
+    float acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+#pragma unroll 4
+    for (int64_t r = rl; r < p.rows; r += RL) {
+      float g[8], h[8];
+      widen8(load8<DK>(p.dy, r * p.lddy + c), g);
+      widen8(load8<HK>(p.h, r * p.ldh + c), h);
+      const float rstd = p.rstd[r];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(g[k], h[k] * rstd, acc[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) red[rl][cl * 8 + k] = acc[k];
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      float v = red[0][threadIdx.x];
+#pragma unroll
+      for (int i = 1; i < RL; ++i) v += red[i][threadIdx.x];
+      p.dw[blockIdx.x * 64 + threadIdx.x] = v;
+    }
+    return;
+  }
   const int t = threadIdx.x % RT;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / RT;
+  const int64_t row = (int64_t)(blockIdx.x - col_wgs) * ROWS + threadIdx.x / RT;
   if (row >= p.rows) return;  // RT = 64 only: whole waves, and no barrier follows
   const int chunks = (int)(p.cols / 8);
   const float rstd = p.rstd[row];
-  float u[C][8], n[C][8];
-  float s = 0.0f;
+  Raw8<DK> dy[C];
+  Raw8<HK> h[C], dh[C];
+  float w[C][8], s = 0.0f;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int ch = i * RT + t;
     if (ch < chunks) {
-      float w[8];
-      widen8(load8<DK>(p.dy, row * p.lddy + 8 * ch), u[i]);
-      widen8(load8<HK>(p.h, row * p.ldh + 8 * ch), n[i]);
-      load_w8(p.w, 8 * ch, w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        n[i][k] *= rstd;
-        u[i][k] *= w[k];
-        s = __builtin_fmaf(u[i][k], n[i][k], s);
-      }
+      dy[i] = load8<DK>(p.dy, row * p.lddy + 8 * ch);
+      h[i] = load8<HK>(p.h, row * p.ldh + 8 * ch);
+      dh[i] = load_dh8<HK>(p, row, 8 * ch);
+      load_w8(p.w, 8 * ch, w[i]);
     }
   }
-  s = row_sum<RT>(s, red) / (float)p.cols;
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if (i * RT + t < chunks) s += row_part8<DK, HK>(dy[i], h[i], w[i], rstd);
+  s = row_sum<RT>(s, &red[0][0]) / (float)p.cols;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int ch = i * RT + t;
-    if (ch < chunks) {
-      float d[8];
+    if (ch < chunks) store_dx8<DK, HK>(p, dy[i], h[i], dh[i], w[i], rstd, s, row * p.cols + 8 * ch);
+  }
+}
+
+// Many rows: every team of RT threads takes rows team, team + teams, ...; its
+// threads keep the same columns throughout, so w and the columns' sums of dy * n
+// stay in registers and every input is read once. The next row is loaded
+// before this row's reduction; two chunks per thread of FP32 rows do not all
+// fit 128 registers, so there dh is loaded with its own row and, where dy is
+// FP32 too, h as well, and w is read again for every row (from L2). A workgroup writes its
+// columns' sums as one partial row (its four teams' added through LDS where
+// RT = 64).
+template <int DK, int HK, int RT, int C>
+__global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const NormBwdArgs p) {
+  constexpr int NT = RT < 256 ? 256 : RT, TEAMS = NT / RT;
+  __shared__ float red[2][RT / 64];
+  __shared__ float sums[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? 512 : 1];
+  constexpr int BYTES = InKind<DK>::kBytes + 2 * InKind<HK>::kBytes;
+  constexpr bool DH_AHEAD = C == 1 || BYTES <= 6, KEEP_W = C == 1 || BYTES <= 10, H_AHEAD = KEEP_W;
+  const int t = threadIdx.x % RT, team = threadIdx.x / RT;
+  const int64_t teams = (int64_t)gridDim.x * TEAMS;
+  const int chunks = (int)(p.cols / 8);
+  float w[C][8], acc[C][8];
+  Raw8<DK> dy[C];
+  Raw8<HK> h[C], dh[C];
+  float rstd = 0.0f;
+  auto load_row = [&](int64_t row, Raw8<DK>(&dy)[C], Raw8<HK>(&h)[C], Raw8<HK>(&dh)[C], float& rstd) {
+    rstd = p.rstd[row];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] = 0.0f;
-      if (p.dh) widen8(load8<HK>(p.dh, row * p.lddh + 8 * ch), d);
+    for (int i = 0; i < C; ++i) {
+      const int ch = i * RT + t;
+      if (ch < chunks) {
+        dy[i] = load8<DK>(p.dy, row * p.lddy + 8 * ch);
+        if (H_AHEAD) h[i] = load8<HK>(p.h, row * p.ldh + 8 * ch);
+        if (DH_AHEAD) dh[i] = load_dh8<HK>(p, row, 8 * ch);
+      }
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * TEAMS + team;
+  if (row < p.rows) load_row(row, dy, h, dh, rstd);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] = __builtin_fmaf(rstd, u[i][k] - n[i][k] * s, d[k]);
-      store8<HK>(p.dx, row * p.cols + 8 * ch, round8<HK>(d));
+  for (int i = 0; i < C; ++i) {
+    const int ch = i * RT + t;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
+    if (KEEP_W && ch < chunks) load_w8(p.w, 8 * ch, w[i]);
+  }
+  for (int it = 0; row < p.rows; row += teams, ++it) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int ch = i * RT + t;
+      if (ch < chunks) {
+        if (!KEEP_W) load_w8(p.w, 8 * ch, w[i]);
+        if (!H_AHEAD) h[i] = load8<HK>(p.h, row * p.ldh + 8 * ch);
+        if (!DH_AHEAD) dh[i] = load_dh8<HK>(p, row, 8 * ch);
+        float g[8], n[8];
+        widen8(dy[i], g);
+        widen8(h[i], n);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          n[k] *= rstd;
+          s = __builtin_fmaf(g[k] * w[i][k], n[k], s);
+          acc[i][k] = __builtin_fmaf(g[k], n[k], acc[i][k]);
+        }
+      }
+    }
+    Raw8<DK> dy1[C];
+    Raw8<HK> h1[C], dh1[C];
+    float rstd1 = 0.0f;
+    const bool more = row + teams < p.rows;
+    if (more) load_row(row + teams, dy1, h1, dh1, rstd1);
+    // two areas in turn: a wave writes one again only after the other's barrier
+    s = row_sum<RT>(s, red[it & 1]) / (float)p.cols;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int ch = i * RT + t;
+      if (ch < chunks) {
+        if (!KEEP_W) load_w8(p.w, 8 * ch, w[i]);
+        store_dx8<DK, HK>(p, dy[i], h[i], dh[i], w[i], rstd, s, row * p.cols + 8 * ch);
+      }
+    }
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        dy[i] = dy1[i];
+        if (H_AHEAD) h[i] = h1[i];
+        if (DH_AHEAD) dh[i] = dh1[i];
+      }
+      rstd = rstd1;
+    }
+  }
+  float* const part = p.ws + (int64_t)blockIdx.x * p.cols;
+  if constexpr (TEAMS > 1) {
+    static_assert(C == 1 && RT * 8 <= 512, "a team's columns fit its row of sums");
+    if (t < chunks) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sums[team][8 * t + k] = acc[0][k];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < (int)p.cols; c += NT) {
+      float v = sums[0][c];
+#pragma unroll
+      for (int i = 1; i < TEAMS; ++i) v += sums[i][c];
+      part[c] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int ch = i * RT + t;
+      if (ch < chunks) store8<0>(part, 8 * ch, round8<0>(acc[i]));
     }
   }
 }
 
-// The same for rows longer than a workgroup's registers, read twice.
+// Rows longer than the registers of a workgroup hold: dx with the row read
+// twice, the columns' sums by rmsnorm_bwd_cols.
 template <int DK, int HK>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_rows_long(const NormBwdArgs p) {
   constexpr int RT = 1024;
@@ -244,31 +407,17 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_rows_long(const NormBwdArgs 
   const int chunks = (int)(p.cols / 8);
   const float rstd = p.rstd[row];
   float s = 0.0f;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int ch = threadIdx.x; ch < chunks; ch += RT) {
-      float u[8], n[8], w[8];
-      widen8(load8<DK>(p.dy, row * p.lddy + 8 * ch), u);
-      widen8(load8<HK>(p.h, row * p.ldh + 8 * ch), n);
-      load_w8(p.w, 8 * ch, w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        n[k] *= rstd;
-        u[k] *= w[k];
-      }
-      if (pass == 0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s = __builtin_fmaf(u[k], n[k], s);
-      } else {
-        float d[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = 0.0f;
-        if (p.dh) widen8(load8<HK>(p.dh, row * p.lddh + 8 * ch), d);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = __builtin_fmaf(rstd, u[k] - n[k] * s, d[k]);
-        store8<HK>(p.dx, row * p.cols + 8 * ch, round8<HK>(d));
-      }
-    }
-    if (pass == 0) s = row_sum<RT>(s, red) / (float)p.cols;
+  for (int ch = threadIdx.x; ch < chunks; ch += RT) {
+    float w[8];
+    load_w8(p.w, 8 * ch, w);
+    s += row_part8<DK, HK>(load8<DK>(p.dy, row * p.lddy + 8 * ch), load8<HK>(p.h, row * p.ldh + 8 * ch), w, rstd);
+  }
+  s = row_sum<RT>(s, red) / (float)p.cols;
+  for (int ch = threadIdx.x; ch < chunks; ch += RT) {
+    float w[8];
+    load_w8(p.w, 8 * ch, w);
+    store_dx8<DK, HK>(p, load8<DK>(p.dy, row * p.lddy + 8 * ch), load8<HK>(p.h, row * p.ldh + 8 * ch),
+                      load_dh8<HK>(p, row, 8 * ch), w, rstd, s, row * p.cols + 8 * ch);
   }
 }
 
@@ -304,34 +453,70 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_cols(const NormBwdArgs p, flo
   }
 }
 
-// Row ranges of the column sums: about 1024 workgroups, at least 16 rows each.
-int64_t bwd_ranges(int64_t rows, int64_t cols) {
-  const int64_t col_groups = (cols + 511) / 512;
-  const int64_t r = 1024 / col_groups, most = (rows + 15) / 16;
-  return r < 1 ? 1 : r < most ? r : most;
+// The backward pass's form and its number of partial rows of dw.
+constexpr int64_t kLongCols = 16384;  // what rmsnorm_bwd_many holds
+constexpr int64_t kFewRows = 128;
+
+struct BwdPlan {
+  bool few;
+  int rt;           // threads per row
+  int64_t partial;  // partial rows (one: the sums go straight to dw)
+};
+
+BwdPlan bwd_plan(int64_t rows, int64_t cols) {
+  BwdPlan b;
+  b.rt = cols <= 512 ? 64 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
+  b.few = cols <= kLongCols && rows <= kFewRows;
+  if (b.few) {
+    b.partial = 1;
+  } else if (cols <= kLongCols) {
+    // 1024 threads per CU
+    const int64_t wg_rows = b.rt < 256 ? 256 / b.rt : 1, wgs = 256 * (1024 / (b.rt < 256 ? 256 : b.rt));
+    b.partial = std::min<int64_t>((rows + wg_rows - 1) / wg_rows, wgs);
+  } else {
+    // about 1024 workgroups of rmsnorm_bwd_cols, at least 16 rows each
+    b.partial = std::max<int64_t>(1, std::min<int64_t>(1024 / ((cols + 511) / 512), (rows + 15) / 16));
+  }
+  return b;
 }
 
 template <int DK, int HK, int RT, int C>
-void launch_bwd_rows(const NormBwdArgs& p, hipStream_t stream) {
-  constexpr int ROWS = RT < 256 ? 256 / RT : 1;
-  hipLaunchKernelGGL((rmsnorm_bwd_rows<DK, HK, RT, C>), dim3((unsigned)((p.rows + ROWS - 1) / ROWS)),
-                     dim3(RT < 256 ? 256 : RT), 0, stream, p);
+void launch_bwd(const NormBwdArgs& p, const BwdPlan& b, hipStream_t stream) {
+  constexpr int NT = RT < 256 ? 256 : RT, ROWS = NT / RT;
+  if (b.few) {
+    const int col_wgs = (int)(p.cols / 64);
+    hipLaunchKernelGGL((rmsnorm_bwd_few<DK, HK, RT, C>), dim3((unsigned)(col_wgs + (p.rows + ROWS - 1) / ROWS)), dim3(NT), 0,
+                       stream, p, col_wgs);
+  } else {
+    hipLaunchKernelGGL((rmsnorm_bwd_many<DK, HK, RT, C>), dim3((unsigned)b.partial), dim3(NT), 0, stream, p);
+  }
 }
 
 template <int DK, int HK>
 hipError_t launch_norm_bwd_k(const NormBwdArgs& p, hipStream_t stream) {
-  // the column sums first: dx may be written over dh, never over dy or h
-  const int64_t ranges = bwd_ranges(p.rows, p.cols), col_groups = (p.cols + 511) / 512;
-  hipLaunchKernelGGL((rmsnorm_bwd_cols<DK, HK>), dim3((unsigned)(col_groups * ranges)), dim3(256), 0, stream, p,
-                     ranges > 1 ? p.ws : p.dw, (int)col_groups, (int)ranges);
-  if (p.cols <= 512) launch_bwd_rows<DK, HK, 64, 1>(p, stream);
-  else if (p.cols <= 2048) launch_bwd_rows<DK, HK, 256, 1>(p, stream);
-  else if (p.cols <= 8192) launch_bwd_rows<DK, HK, 1024, 1>(p, stream);
-  else if (p.cols <= 16384) launch_bwd_rows<DK, HK, 1024, 2>(p, stream);
-  else hipLaunchKernelGGL((rmsnorm_bwd_rows_long<DK, HK>), dim3((unsigned)p.rows), dim3(1024), 0, stream, p);
+  const BwdPlan b = bwd_plan(p.rows, p.cols);
+  NormBwdArgs q = p;
+  const bool direct = b.partial == 1;
+  if (direct) q.ws = p.dw;  // one partial row is dw itself
+  if (p.cols > kLongCols) {
+    const int64_t col_groups = (p.cols + 511) / 512;
+    hipLaunchKernelGGL((rmsnorm_bwd_cols<DK, HK>), dim3((unsigned)(col_groups * b.partial)), dim3(256), 0, stream, q, q.ws,
+                       (int)col_groups, (int)b.partial);
+    hipLaunchKernelGGL((rmsnorm_bwd_rows_long<DK, HK>), dim3((unsigned)p.rows), dim3(1024), 0, stream, q);
+  } else if (b.rt == 64) {
+    launch_bwd<DK, HK, 64, 1>(q, b, stream);
+  } else if (b.rt == 256) {
+    launch_bwd<DK, HK, 256, 1>(q, b, stream);
+  } else if (b.rt == 512) {
+    launch_bwd<DK, HK, 512, 1>(q, b, stream);
+  } else if (p.cols <= 8192) {
+    launch_bwd<DK, HK, 1024, 1>(q, b, stream);
+  } else {
+    launch_bwd<DK, HK, 1024, 2>(q, b, stream);
+  }
   const hipError_t err = hipGetLastError();
-  if (err != hipSuccess || ranges == 1) return err;
-  return launch_column_sum(p.ws, ranges, p.cols, p.dw, stream);
+  if (err != hipSuccess || direct) return err;
+  return launch_column_sum(p.ws, b.partial, p.cols, p.dw, stream);
 }
 
 template <int DK>
@@ -344,25 +529,36 @@ hipError_t launch_norm_bwd_d(const NormBwdArgs& p, hipStream_t stream) {
   }
 }
 
-// 64 columns per workgroup, four groups of 64 threads taking the partial rows
-// in turn (eight loads in flight each), then added through LDS in group order.
-__global__ __launch_bounds__(256) void column_sum(const float* __restrict__ part, int64_t n, int64_t cols,
-                                                  float* __restrict__ out) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  float s = 0.0f;
+// 64 columns per workgroup: 16 lanes of four columns, 64 groups of lanes taking
+// the partial rows in turn (eight loads in flight each), then added over the
+// wave's four groups by shuffles and over the 16 waves through LDS, in order.
+__global__ __launch_bounds__(1024) void column_sum(const float* __restrict__ part, int64_t n, int64_t cols,
+                                                   float* __restrict__ out) {
+  __shared__ float red[16][64];
+  const int cl = threadIdx.x & 15, grp = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+  const float* src = part + (int64_t)blockIdx.x * 64 + cl * 4;
+  v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-  for (int64_t r = grp; r < n; r += 4) s += part[r * cols + c];
-  red[grp][lane] = s;
+  for (int64_t r = grp; r < n; r += 64) s += *reinterpret_cast<const v4f*>(src + r * cols);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    s[k] += __shfl_xor(s[k], 16, 64);
+    s[k] += __shfl_xor(s[k], 32, 64);
+    if ((threadIdx.x & 63) < 16) red[wave][cl * 4 + k] = s[k];
+  }
   __syncthreads();
-  if (grp == 0) out[c] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+  if (threadIdx.x < 64) {
+    float v = red[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += red[i][threadIdx.x];
+    out[(int64_t)blockIdx.x * 64 + threadIdx.x] = v;
+  }
 }
 
 }  // namespace
 
 hipError_t launch_column_sum(const float* part, int64_t n, int64_t cols, float* out, hipStream_t stream) {
-  hipLaunchKernelGGL(column_sum, dim3((unsigned)(cols / 64)), dim3(256), 0, stream, part, n, cols, out);
+  hipLaunchKernelGGL(column_sum, dim3((unsigned)(cols / 64)), dim3(1024), 0, stream, part, n, cols, out);
   return hipGetLastError();
 }
 
@@ -376,8 +572,8 @@ hipError_t launch_norm(const NormArgs& p, hipStream_t stream) {
 }
 
 int64_t norm_bwd_workspace(int64_t rows, int64_t cols) {
-  const int64_t ranges = bwd_ranges(rows, cols);
-  return ranges > 1 ? ranges * cols * (int64_t)sizeof(float) : 0;
+  const int64_t n = bwd_plan(rows, cols).partial;
+  return n > 1 ? n * cols * (int64_t)sizeof(float) : 0;
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& p, hipStream_t stream) {
