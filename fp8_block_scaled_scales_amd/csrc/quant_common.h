@@ -161,13 +161,16 @@ struct Raw8 {
 };
 
 // p: base of a matrix of kind K; e: index of the first element (the address
-// is 16-byte aligned).
-template <int K>
+// is 16-byte aligned). ONCE: data read once and larger than the caches.
+template <int K, bool ONCE = false>
 __device__ __forceinline__ Raw8<K> load8(const void* p, int64_t e) {
   Raw8<K> r;
   const v4u* src = reinterpret_cast<const v4u*>(static_cast<const char*>(p) + e * InKind<K>::kBytes);
 #pragma unroll
-  for (int i = 0; i < InKind<K>::kBytes / 2; ++i) r.w[i] = src[i];
+  for (int i = 0; i < InKind<K>::kBytes / 2; ++i) {
+    if constexpr (ONCE) r.w[i] = __builtin_nontemporal_load(src + i);
+    else r.w[i] = src[i];
+  }
   return r;
 }
 
