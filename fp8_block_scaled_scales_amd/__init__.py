@@ -122,6 +122,13 @@ def load_library(path: str):
 
 
 _lib = load_library(LIB_PATH)
+try:
+    from . import _binding  # the short way into the calls that serve a few tokens
+except ImportError as e:
+    raise ImportError("_binding.so is not built for this torch (run fp8_block_scaled_scales_amd.build.build()): %s" % e)
+_binding.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
+    "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward", "dg_rmsnorm_backward_workspace", "dg_epilogue_backward_fp8",
+    "dg_epilogue_backward_workspace", "dg_gemm_fp8_residual")))
 lib = _lib  # raw ctypes handle, for tests that exercise the C ABI directly
 
 
@@ -493,9 +500,11 @@ def dg_quantize_fp8_rows_typed(x, gran: int = 128, fmt: int = DG_FMT_E4M3, q=Non
 _F32 = (torch.float32,)
 _BF16 = (torch.bfloat16,)
 
-# The calls below take a few microseconds on the GPU for a few tokens. The
-# current stream's and device's raw forms cost 0.06 and 0.09 us, the public
-# objects 1.7 and 0.2 us.
+# The calls below take a few microseconds on the GPU for a few tokens. Where
+# every tensor is given and right, _binding checks and launches them; the code
+# here does the rest: it allocates what is not given, takes a given stream and
+# names what is wrong. The current stream's and device's raw forms cost 0.06 and
+# 0.09 us, the public objects 1.7 and 0.2 us.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -567,6 +576,13 @@ def dg_gemm_fp8_residual(a, b, sa, sb, res=None, out=None, gran: int = 128, layo
     itself. act: one of the five DG_ACT_* codes. pre: optional [M,N] bfloat16 that
     receives C + bias, for dg_epilogue_backward_fp8.
     """
+    if stream is None:
+        rc = _binding.gemm_residual(a, b, sa, sb, res, out, gran, layout, gran if sa_rows is None else sa_rows, fmt_a, fmt_b, bias,
+                                    act, pre)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_gemm_fp8_residual")
+            return out
     if act not in (DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU, DG_ACT_SILU, DG_ACT_GELU_TANH):
         raise ValueError("act must be one of the DG_ACT_* codes")
     kind, pitch = 0, 0
@@ -600,6 +616,12 @@ def dg_rmsnorm_quantize_fp8(x, res, weight, eps: float = 1e-6, gran: int = 128, 
     codes, or that float8 dtype) and scales [rows, cols/gran] are what
     dg_gemm_fp8_residual takes as a and sa with sa_rows = 1.
     """
+    if stream is None:
+        rc = _binding.rmsnorm_quantize(x, res, weight, eps, gran, fmt, h, y, rstd, q, scales)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_rmsnorm_quantize_fp8")
+            return q, scales, x if res is None else h
     rows, cols = shape = _matrix(x, "x")
     dev = x.device
     if gran not in _GRANS or cols % gran:
@@ -635,6 +657,12 @@ def dg_rmsnorm_backward(dy, h, rstd, weight, dh=None, dx=None, dweight=None, wor
     of x and of the residual alike, of h's dtype; dweight is [cols] float32. workspace:
     a uint8 tensor of dg_rmsnorm_backward_workspace(rows, cols) bytes (allocated when None).
     """
+    if stream is None:
+        rc = _binding.rmsnorm_backward(dy, h, rstd, weight, dh, dx, dweight, workspace)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_rmsnorm_backward")
+            return dx, dweight
     rows, cols = shape = _matrix(dy, "dy")
     dev = dy.device
     if cols % 64 or not rows or not cols:
@@ -674,13 +702,19 @@ def dg_epilogue_backward_fp8(dout, pre, act: int, gran: int = 128, block_rows: i
     given, receive the FP32 gradient rounded once and its sum over the rows.
     workspace: a uint8 tensor of dg_epilogue_backward_workspace(...) bytes (allocated when None).
     """
+    block_rows = gran if block_rows is None else block_rows
+    if stream is None:
+        rc = _binding.epilogue_backward(dout, pre, act, gran, block_rows, fmt, dz, dbias, q, scales, workspace)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_epilogue_backward_fp8")
+            return q, scales
     rows, cols = shape = _matrix(dout, "dout")
     dev = dout.device
     if gran not in _GRANS or cols % gran or not rows or not cols:
         raise ValueError("dout must have rows and columns, and gran must be 64, 128 or 256 and divide cols")
     if fmt not in _FP8_OF:
         raise ValueError("fmt must be DG_FMT_E4M3 or DG_FMT_E5M2")
-    block_rows = gran if block_rows is None else block_rows
     if block_rows not in (gran, 1):
         raise ValueError("block_rows must be gran (g x g blocks) or 1 (per-row factors)")
     if act not in (DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU, DG_ACT_SILU, DG_ACT_GELU_TANH):

@@ -1,4 +1,5 @@
-"""Compile the HIP library ``libdg.so`` for gfx950 in-tree with hipcc.
+"""Compile the HIP library ``libdg.so`` for gfx950 in-tree with hipcc, and the
+host-only tensor binding ``_binding.so`` with g++ against the installed torch.
 
 Used by ``__graft_entry__.build()``; also runnable as ``python -m
 fp8_block_scaled_scales_amd.build``. Always recompiles.
@@ -43,6 +44,24 @@ FLAGS = [
 VARIANTS = {"libdg.so": [], "libdg_sync.so": ["-DDG_EXTRA_SYNC"]}
 LINK = ["--offload-arch=gfx950", "-shared", "-fPIC", "-Wl,-Bsymbolic"]
 
+# The tensor binding (csrc/binding.cpp): host code only, so g++; its torch
+# libraries are the ones the interpreter has loaded by then.
+BINDING = os.path.join(HERE, "_binding.so")
+
+
+def binding_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] +
+            ["-I" + d for d in cpp_extension.include_paths() + [os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+                                                                sysconfig.get_paths()["include"]]] +
+            [os.path.join(CSRC, "binding.cpp"), "-o", out] + ["-L" + d for d in cpp_extension.library_paths()] +
+            ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"])
+
 
 def build(verbose: bool = False, variants=None) -> str:
     """Compile every source of every variant to an object (at most one hipcc
@@ -57,6 +76,9 @@ def build(verbose: bool = False, variants=None) -> str:
             cmd = [HIPCC] + [f for f in FLAGS if f != "-shared"] + VARIANTS[name] + \
                 ["-c", os.path.join(CSRC, src), "-o", obj]
             jobs.append((name, obj, cmd))
+
+    binding_tmp = BINDING + ".tmp" + tag
+    jobs.insert(0, (None, binding_tmp, binding_command(binding_tmp)))
 
     def compile_one(cmd):
         if verbose:
@@ -83,6 +105,7 @@ def build(verbose: bool = False, variants=None) -> str:
                 sys.stderr.write(res.stdout + res.stderr)
                 raise RuntimeError("hipcc failed linking " + name)
             os.replace(tmp, lib)
+        os.replace(binding_tmp, BINDING)
     finally:
         for _, obj, _ in jobs:
             if os.path.exists(obj):

@@ -422,6 +422,58 @@ def test_given_stream_allocates_there(dg):
         del junk
 
 
+def test_current_stream(dg):
+    """Without a stream argument a call runs on torch's current stream: it is captured there, and outputs and
+    workspaces left to the call (the Python way) or given (the short way) give the same bits."""
+    t = _buffers(dg, 200, 512, 640, 31)
+    args = (t["y"], t["h"], t["rstd"], t["w"])
+    say("the current stream")
+    _layer(dg, t)
+    torch.cuda.synchronize()
+    want = {k: t[k].clone() for k in OUTPUTS}
+    for k in OUTPUTS:
+        t[k].zero_()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        _layer(dg, t)
+    torch.cuda.synchronize()
+    assert not t["q"].any()  # captured, not run
+    graph.replay()
+    torch.cuda.synchronize()
+    for k in OUTPUTS:
+        assert torch.equal(t[k].view(torch.uint8), want[k].view(torch.uint8)), k
+    dx, dw = dg.dg_rmsnorm_backward(*args, dh=t["x"])
+    assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dw"])
+    dw2 = torch.empty_like(dw)
+    dx2, _ = dg.dg_rmsnorm_backward(*args, dh=t["x"], dx=torch.empty_like(dx), dweight=dw2)  # the workspace left to the call
+    assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
+def test_short_way_refuses_the_same(dg):
+    """A status from a call whose tensors are right raises; wrong tensors are named by the Python checks."""
+    x, w = torch.ones(4, 256, dtype=BF16, device=DEV), torch.ones(256, device=DEV)
+    h, q, s = torch.empty_like(x), torch.empty(4, 256, dtype=torch.uint8, device=DEV), torch.empty(4, 2, device=DEV)
+    say("refusals on the GPU")
+    with pytest.raises(dg.DGArgumentError):
+        dg.dg_rmsnorm_quantize_fp8(x, x, w, 1e-6, h=h, q=q, scales=s, y=h)  # two outputs in one place
+    with pytest.raises(dg.DGArgumentError):
+        dg.dg_rmsnorm_quantize_fp8(x, x, w, -1.0, h=h, q=q, scales=s)
+    with pytest.raises(ValueError, match="scales has shape"):
+        dg.dg_rmsnorm_quantize_fp8(x, x, w, 1e-6, h=h, q=q, scales=s[:3])
+    with pytest.raises(ValueError, match="q has dtype"):
+        dg.dg_rmsnorm_quantize_fp8(x, x, w, 1e-6, h=h, q=q.view(torch.float8_e5m2), scales=s)
+    with pytest.raises(ValueError, match="weight is on"):
+        dg.dg_rmsnorm_quantize_fp8(x, x, w.cpu(), 1e-6, h=h, q=q, scales=s)
+    with pytest.raises(dg.DGArgumentError):  # a row pitch that is no multiple of 16 bytes
+        wide = torch.ones(4, 257, dtype=BF16, device=DEV)
+        dg.dg_rmsnorm_quantize_fp8(wide[:, :256], x, w, 1e-6, h=h, q=q, scales=s)
+    many = torch.ones(1000, 256, dtype=BF16, device=DEV)
+    with pytest.raises(dg.DGArgumentError):  # a workspace that is too small
+        dg.dg_rmsnorm_backward(many, many, torch.ones(1000, device=DEV), w, dx=torch.empty_like(many),
+                               dweight=torch.empty_like(w), workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
 def test_offsets_past_32_bits(dg):
     """More than 2^32 elements: the last rows against the reference on those rows."""
     rows, cols, n = (1 << 19) + 5, 8192, 4
