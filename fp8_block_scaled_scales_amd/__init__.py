@@ -101,7 +101,9 @@ def load_library(path: str):
     fmt, act, kind, f32 = ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float
     lib.dg_gemm_fp8_residual.restype = ctypes.c_int
     lib.dg_gemm_fp8_residual.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
-                                         fmt, fmt, vp, act, vp, kind, i64, vp, vp]
+                                         fmt, fmt, vp, act, vp, kind, i64, vp, vp, i64, vp]
+    lib.dg_gemm_fp8_residual_workspace.restype = i64
+    lib.dg_gemm_fp8_residual_workspace.argtypes = [i64, i64, i64, ctypes.c_int, ctypes.c_int]
     lib.dg_rmsnorm_quantize_fp8.restype = ctypes.c_int
     lib.dg_rmsnorm_quantize_fp8.argtypes = [vp, kind, i64, vp, kind, i64, vp, f32, i64, i64, ctypes.c_int, fmt, vp, vp,
                                             vp, vp, vp, vp]
@@ -128,7 +130,7 @@ except ImportError as e:
     raise ImportError("_binding.so is not built for this torch (run fp8_block_scaled_scales_amd.build.build()): %s" % e)
 _binding.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
     "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward", "dg_rmsnorm_backward_workspace", "dg_epilogue_backward_fp8",
-    "dg_epilogue_backward_workspace", "dg_gemm_fp8_residual")))
+    "dg_epilogue_backward_workspace", "dg_gemm_fp8_residual", "dg_gemm_fp8_residual_workspace")))
 lib = _lib  # raw ctypes handle, for tests that exercise the C ABI directly
 
 
@@ -568,17 +570,19 @@ def _matrix(t, name):
 
 def dg_gemm_fp8_residual(a, b, sa, sb, res=None, out=None, gran: int = 128, layout: int = DG_LAYOUT_NT,
                          sa_rows: int | None = None, fmt_a: int = DG_FMT_E4M3, fmt_b: int = DG_FMT_E4M3, bias=None,
-                         act: int = DG_ACT_NONE, pre=None, stream=None):
+                         act: int = DG_ACT_NONE, pre=None, workspace=None, stream=None):
     """out = bf16(act(C + bias) + res), the product with a residual and any activation in its epilogue.
 
     a, b, sa, sb, gran, layout, sa_rows, formats and bias as dg_gemm_fp8_ws. res: [M,N]
     float32, bfloat16 or float16, rows contiguous (any pitch), or None; it may be out
     itself. act: one of the five DG_ACT_* codes. pre: optional [M,N] bfloat16 that
-    receives C + bias, for dg_epilogue_backward_fp8.
+    receives C + bias, for dg_epilogue_backward_fp8. workspace: a uint8 tensor of
+    dg_gemm_fp8_residual_workspace(...) bytes, which only few output tiles with a long K
+    use (allocated when None).
     """
     if stream is None:
         rc = _binding.gemm_residual(a, b, sa, sb, res, out, gran, layout, gran if sa_rows is None else sa_rows, fmt_a, fmt_b, bias,
-                                    act, pre)
+                                    act, pre, workspace)
         if rc is not None:
             if rc:
                 _raise(rc, "dg_gemm_fp8_residual")
@@ -598,10 +602,20 @@ def dg_gemm_fp8_residual(a, b, sa, sb, res=None, out=None, gran: int = 128, layo
     M, N, K, sa_rows, dev = _ws_args(a, b, sa, sb, out, gran, layout, sa_rows, fmt_a, fmt_b, bias, DG_ACT_NONE, more)
     if out is None:
         out = _out(None, "out", _BF16, (M, N), dev, stream)
+    need = _lib.dg_gemm_fp8_residual_workspace(M, N, K, gran, layout)
+    ws = _workspace(workspace, need, dev, stream) if need > 0 else None
     _launch(_lib.dg_gemm_fp8_residual, "dg_gemm_fp8_residual", dev, stream, a.data_ptr(), b.data_ptr(), sa.data_ptr(),
             sb.data_ptr(), out.data_ptr(), M, N, K, gran, layout, sa_rows, fmt_a, fmt_b, _ptr(bias), act, _ptr(res),
-            kind, pitch, _ptr(pre))
+            kind, pitch, _ptr(pre), _ptr(ws), ws.numel() if need > 0 else 0)
     return out
+
+
+def dg_gemm_fp8_residual_workspace(M: int, N: int, K: int, gran: int = 128, layout: int = DG_LAYOUT_NT) -> int:
+    """Workspace bytes with which dg_gemm_fp8_residual splits K (0 where it does not)."""
+    n = _lib.dg_gemm_fp8_residual_workspace(M, N, K, gran, layout)
+    if n < 0:
+        _raise(n, "dg_gemm_fp8_residual_workspace")
+    return n
 
 
 def dg_rmsnorm_quantize_fp8(x, res, weight, eps: float = 1e-6, gran: int = 128, fmt: int = DG_FMT_E4M3, h=None, y=None,
@@ -752,6 +766,7 @@ __all__ = ["dg_gemm_fp8_nt", "dg_gemm_fp8_nt_fmt", "dg_gemm_fp8_nt_epi", "dg_gem
            "DG_ACT_RELU", "DG_ACT_GELU", "dg_quantize_e4m3_blocks", "dg_quantize_fp8_blocks", "dg_quantize_fp8_rows",
            "dg_quantize_fp8_blocks_typed", "dg_quantize_fp8_rows_typed", "DG_IN_F32", "DG_IN_BF16", "DG_IN_F16",
            "dg_query_tile", "dg_strerror", "dg_version", "DGError", "DGArgumentError", "DG_OK", "DG_EINVAL",
-           "dg_gemm_fp8_residual", "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward", "dg_rmsnorm_backward_workspace",
+           "dg_gemm_fp8_residual", "dg_gemm_fp8_residual_workspace", "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward",
+           "dg_rmsnorm_backward_workspace",
            "dg_epilogue_backward_fp8", "dg_epilogue_backward_workspace", "DG_ACT_SILU", "DG_ACT_GELU_TANH",
            "DG_EALIGN", "DG_EUNSUPPORTED", "DG_ELAUNCH", "DG_FMT_E4M3", "DG_FMT_E5M2", "DG_MAX_DIM", "LIB_PATH"]

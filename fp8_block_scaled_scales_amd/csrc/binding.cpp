@@ -30,6 +30,7 @@ decltype(&dg_rmsnorm_backward_workspace) g_norm_bwd_ws;
 decltype(&dg_epilogue_backward_fp8) g_epi_bwd;
 decltype(&dg_epilogue_backward_workspace) g_epi_bwd_ws;
 decltype(&dg_gemm_fp8_residual) g_gemm;
+decltype(&dg_gemm_fp8_residual_workspace) g_gemm_ws;
 
 // What one call's arguments are checked against: dev is the first tensor's
 // device; ok turns false at the first argument that is not plainly right.
@@ -236,11 +237,11 @@ PyObject* epilogue_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// a, b, sa, sb, res, out, gran, layout, sa_rows, fmt_a, fmt_b, bias, act, pre
+// a, b, sa, sb, res, out, gran, layout, sa_rows, fmt_a, fmt_b, bias, act, pre, workspace
 PyObject* gemm_residual(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     Call k;
-    const at::Tensor* A = n == 14 ? k.first(a[0]) : nullptr;
+    const at::Tensor* A = n == 15 ? k.first(a[0]) : nullptr;
     const at::Tensor* B = A ? k.tensor(a[1]) : nullptr;
     if (!B || B->dim() != 2) Py_RETURN_NONE;
     const int64_t g = k.integer(a[6]), layout = k.integer(a[7]), sr = k.integer(a[8]), fa = k.integer(a[9]),
@@ -259,21 +260,28 @@ PyObject* gemm_residual(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* bias = k.vec_or_none(a[11], N);
     void* pre = k.mat_or_none(a[13], c10::ScalarType::BFloat16, M, N);
     if (!k.ok) Py_RETURN_NONE;
+    const int64_t need = g_gemm_ws(M, N, K, (int)g, (int)layout);
+    if (need < 0) Py_RETURN_NONE;
+    at::Tensor ws;
+    if (need) ws = k.workspace(a[14], need);
+    if (!k.ok) Py_RETURN_NONE;
     return status(g_gemm(pa, pb, (const float*)sa, (const float*)sb, out, M, N, K, (int)g, (int)layout, (int)sr, (int)fa,
-                         (int)fb, (const float*)bias, (int)act, res.p, res.kind, res.pitch, pre, k.stream()));
+                         (int)fb, (const float*)bias, (int)act, res.p, res.kind, res.pitch, pre,
+                         need ? ws.data_ptr() : nullptr, need ? ws.numel() : 0, k.stream()));
   });
 }
 
 // The addresses of the library's entry points, in the order below.
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long p[6];
-  if (!PyArg_ParseTuple(args, "KKKKKK", &p[0], &p[1], &p[2], &p[3], &p[4], &p[5])) return nullptr;
+  unsigned long long p[7];
+  if (!PyArg_ParseTuple(args, "KKKKKKK", &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6])) return nullptr;
   g_norm = (decltype(g_norm))p[0];
   g_norm_bwd = (decltype(g_norm_bwd))p[1];
   g_norm_bwd_ws = (decltype(g_norm_bwd_ws))p[2];
   g_epi_bwd = (decltype(g_epi_bwd))p[3];
   g_epi_bwd_ws = (decltype(g_epi_bwd_ws))p[4];
   g_gemm = (decltype(g_gemm))p[5];
+  g_gemm_ws = (decltype(g_gemm_ws))p[6];
   Py_RETURN_NONE;
 }
 

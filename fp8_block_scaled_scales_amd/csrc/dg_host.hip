@@ -44,6 +44,17 @@ constexpr int64_t kWsFloats = 4ll << 20;  // 16 MB of partial tiles
 // kMaxSplit bounds the second kernel's sum per output.
 constexpr int64_t kSplitMinSteps = 128;
 constexpr int64_t kSplitMin = 8;
+
+// The same bounds for dg_gemm_fp8_residual. With a transposed operand the
+// streaming tiles take its K rows in 32-byte pieces at about half the rate, the
+// 64x64 tiles in 64-byte ones, so a split wins earlier: 19x51x12352 TN 25.2 ->
+// 11.9 us, 565x68x10240 TT 19.9 -> 13.5, 47x19x6656 TT 11.0 -> 9.9; 2x453x3840
+// NN 9.5 -> 9.9. NT: 8x300x8192 9.7 -> 8.2, 64x512x8192 10.4 -> 9.2. The plain
+// calls keep one plan for every layout, so that every layout gives the same
+// bits.
+constexpr int64_t kSplitMinStepsT = 48, kSplitMinStepsR = 64;
+
+int64_t residual_split_steps(int layout) { return layout != DG_LAYOUT_NT ? kSplitMinStepsT : kSplitMinStepsR; }
 constexpr int64_t kMaxSplit = 16;
 
 // Workspace layout of a split-K plan: the FP32 partial tiles,
@@ -159,7 +170,7 @@ double estimate_us(const dg::KernelEntry* e, int64_t M, int64_t N, int64_t K) {
          (double)rounds * (e->round_us + std::max(bytes / (e->cu_gbps * 1e3), flop / (e->cu_tflops * 1e6)));
 }
 
-Plan plan(int64_t M, int64_t N, int64_t K, int sgran, bool split_ok) {
+Plan plan(int64_t M, int64_t N, int64_t K, int sgran, bool split_ok, int64_t split_steps = kSplitMinSteps) {
   Plan p{nullptr, 1, 0};
   const int gran = kernel_gran(sgran);
   const int64_t nsteps = (K + 127) / 128;
@@ -179,7 +190,7 @@ Plan plan(int64_t M, int64_t N, int64_t K, int sgran, bool split_ok) {
       return p;
     }
   }
-  if (split_ok && nsteps >= kSplitMinSteps && split_k().ksplit >= kSplitMin) return p;
+  if (split_ok && nsteps >= split_steps && split_k().ksplit >= kSplitMin) return p;
   // The entry with the least estimated time: small tiles where there are few
   // of them (fewer bytes per CU, more CUs busy), large ones where the
   // arithmetic dominates.
@@ -261,7 +272,7 @@ bool good_pitch(int64_t ld, int64_t cols) { return ld >= cols && ld <= DG_MAX_DI
 // split_ok: few-tile long-K shapes may split K over workgroups, through ws (the
 // caller's, ws_bytes long; none when ws_bytes is 0) or, with use_scratch,
 // through the library's static scratch array. rs: the residual epilogue (null:
-// none), which takes every activation and never splits.
+// none), which takes every activation.
 int gemm(const void* a, const void* b, const float* sa, const float* sb, void* out, int64_t M, int64_t N, int64_t K,
          int gran, int layout, int sa_rows, int fmt_a, int fmt_b, const float* bias, int act, void* stream,
          bool split_ok = false, void* ws = nullptr, int64_t ws_bytes = 0, bool use_scratch = false,
@@ -284,7 +295,8 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
       ((uintptr_t)out & 1))
     return DG_EALIGN;
   // A workspace lets few-tile long-K shapes split K; without one nothing does.
-  Plan pl = plan(M, N, K, gran, split_ok && (ws_bytes > 0 || use_scratch));
+  Plan pl = plan(M, N, K, gran, split_ok && (ws_bytes > 0 || use_scratch),
+                 rs ? residual_split_steps(layout) : kSplitMinSteps);
   if (!pl.e || pl.tiles * pl.ksplit > 0x7fffffff) return DG_EINVAL;
   const int64_t need = workspace_bytes(pl);
   if (ws_bytes > 0 && ws_bytes < need) return DG_EINVAL;
@@ -313,7 +325,7 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
       if (!in_place && overlaps(out, ob, rs->res, rb)) return DG_EINVAL;
       if (overlaps(rs->pre, pb, out, ob) || overlaps(rs->pre, pb, rs->res, rb) || overlaps(rs->pre, pb, a, ab) ||
           overlaps(rs->pre, pb, b, bb) || overlaps(rs->pre, pb, sa, sab) || overlaps(rs->pre, pb, sb, sbb) ||
-          overlaps(rs->pre, pb, bias, biasb))
+          overlaps(rs->pre, pb, bias, biasb) || overlaps(rs->pre, pb, ws, wsb) || overlaps(ws, wsb, rs->res, rb))
         return DG_EINVAL;
     }
   }
@@ -354,7 +366,6 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
   // nothing that the plain forms lack: they run (the same product and rounding)
   const bool form3 = rs && (rs->res || rs->pre || act > DG_ACT_GELU);
   if (form3) {
-    const bool cols8 = N % 8 == 0;
     p.epi.bias = bias;
     p.epi.res = rs->res;
     p.epi.out = static_cast<uint16_t*>(out);
@@ -362,8 +373,6 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
     p.epi.ldres = rs->ldres;
     p.epi.res_kind = rs->res ? rs->res_type : dg::kAbsent;
     p.epi.act = act;
-    p.epi.vec = p.vec_store | (cols8 && ((uintptr_t)rs->pre & 15) == 0 ? 2 : 0) |
-                (((uintptr_t)rs->res & 15) == 0 && (rs->ldres * kind_size(rs->res_type)) % 16 == 0 ? 4 : 0);
   }
   if (log_enabled())
     std::fprintf(stderr,
@@ -732,10 +741,15 @@ int dg_quantize_fp8_rows_typed(const void* x, int in_type, int64_t rows, int64_t
 int dg_gemm_fp8_residual(const void* a, const void* b, const float* sa, const float* sb, void* out, int64_t M,
                          int64_t N, int64_t K, int gran, int layout, int sa_rows, int fmt_a, int fmt_b,
                          const float* bias, int act, const void* res, int res_type, int64_t ldres, void* pre,
-                         void* stream) {
+                         void* workspace, int64_t workspace_bytes, void* stream) {
   const Residual rs{res, res_type, ldres, pre};
-  return gemm(a, b, sa, sb, out, M, N, K, gran, layout, sa_rows, fmt_a, fmt_b, bias, act, stream, false, nullptr, 0,
-              false, &rs);
+  return gemm(a, b, sa, sb, out, M, N, K, gran, layout, sa_rows, fmt_a, fmt_b, bias, act, stream, true, workspace,
+              workspace_bytes, false, &rs);
+}
+
+int64_t dg_gemm_fp8_residual_workspace(int64_t M, int64_t N, int64_t K, int gran, int layout) {
+  if (validate(M, N, K, gran) != DG_OK || validate_layout(M, N, layout) != DG_OK) return DG_EINVAL;
+  return workspace_bytes(plan(M, N, K, gran, true, residual_split_steps(layout)));
 }
 
 int dg_rmsnorm_quantize_fp8(const void* x, int x_type, int64_t ldx, const void* res, int res_type, int64_t ldres,

@@ -8,7 +8,9 @@
 // consecutive outputs of a row: the residual is read and pre and out are
 // written 16 bytes at a time, and the activation is code for eight values, not
 // for every accumulator register, which lets one compiled form take every
-// activation and residual type.
+// activation and residual type. Rows of any pitch and base keep the 16-byte
+// accesses (global memory takes them at any address; the types below carry
+// the elements' own alignment): only the last few columns go one by one.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -29,49 +31,82 @@ struct EpiArgs {
   int64_t ldres;
   int res_kind;       // 0 FP32, 1 BF16, 2 FP16, 3 none
   int act;            // 0 none, 1 ReLU, 2 GELU, 3 SiLU, 4 GELU (tanh form)
-  int vec;            // 16-byte accesses: bit 0 out, bit 1 pre, bit 2 residual
 };
 
-// The residual of NV (4 or 8) outputs from (row, col) on, in FP32; those past
-// column N - 1 are zero. row < M and col < N.
+// Four words at the alignment of the elements they hold.
+typedef v4f v4f_at4 __attribute__((aligned(4)));
+typedef unsigned v2u_at2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef unsigned v4u_at2 __attribute__((ext_vector_type(4), aligned(2)));
+
+// The residual of NV (4 or 8) consecutive outputs as loaded, so that a load
+// long before its use waits for nothing: FP32 words; 16-bit elements two to a
+// word, or one to a word (the low half) where the row ends inside.
 template <int NV>
-__device__ __forceinline__ void load_residual(const EpiArgs& e, int64_t row, int col, int N, float (&r)[NV]) {
-#pragma unroll
-  for (int t = 0; t < NV; ++t) r[t] = 0.0f;
+struct RawResidual {
+  unsigned w[NV];
+};
+
+// From (row, col) on; row < M and col < N.
+template <int NV>
+__device__ __forceinline__ void load_residual(const EpiArgs& e, int64_t row, int col, int N, RawResidual<NV>& r) {
   if (e.res_kind == 3) return;
   const int64_t at = row * e.ldres + col;
-  if ((e.vec & 4) && col + NV <= N) {
+  if (col + NV <= N) {
     if (e.res_kind == 0) {
-      const v4f* src = reinterpret_cast<const v4f*>(static_cast<const float*>(e.res) + at);
+      const float* src = static_cast<const float*>(e.res) + at;
 #pragma unroll
-      for (int t = 0; t < NV; ++t) r[t] = src[t / 4][t % 4];
+      for (int q = 0; q < NV / 4; ++q) {
+        const v4f v = *reinterpret_cast<const v4f_at4*>(src + 4 * q);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) r.w[4 * q + t] = __float_as_uint(v[t]);
+      }
     } else {
-      unsigned w[NV / 2];
       const uint16_t* src = static_cast<const uint16_t*>(e.res) + at;
       if constexpr (NV == 8) {
-        const v4u v = *reinterpret_cast<const v4u*>(src);
+        const v4u v = *reinterpret_cast<const v4u_at2*>(src);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = v[t];
+        for (int t = 0; t < 4; ++t) r.w[t] = v[t];
       } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(src);
-        w[0] = v.x;
-        w[1] = v.y;
-      }
-#pragma unroll
-      for (int t = 0; t < NV / 2; ++t) {
-        const v2h h = __builtin_bit_cast(v2h, w[t]);
-        r[2 * t] = e.res_kind == 1 ? __uint_as_float(w[t] << 16) : (float)h.x;
-        r[2 * t + 1] = e.res_kind == 1 ? __uint_as_float(w[t] & 0xFFFF0000u) : (float)h.y;
+        const v2u_at2 v = *reinterpret_cast<const v2u_at2*>(src);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
       }
     }
   } else {
 #pragma unroll
     for (int t = 0; t < NV; ++t) {
       if (col + t >= N) break;
-      if (e.res_kind == 0) r[t] = static_cast<const float*>(e.res)[at + t];
-      else if (e.res_kind == 1) r[t] = __uint_as_float((unsigned)static_cast<const uint16_t*>(e.res)[at + t] << 16);
-      else r[t] = (float)static_cast<const _Float16*>(e.res)[at + t];
+      r.w[t] = e.res_kind == 0 ? static_cast<const unsigned*>(e.res)[at + t] : static_cast<const uint16_t*>(e.res)[at + t];
     }
+  }
+}
+
+// z += the residual, those outputs past column N - 1 left as they are.
+template <int NV>
+__device__ __forceinline__ void add_residual(const EpiArgs& e, int col, int N, const RawResidual<NV>& r, float (&z)[NV]) {
+  const bool whole = col + NV <= N;
+  auto half = [&](unsigned w) { return (float)__builtin_bit_cast(v2h, w).x; };
+  switch (e.res_kind) {  // the same for the whole launch
+    case 0:
+#pragma unroll
+      for (int t = 0; t < NV; ++t)
+        if (whole || col + t < N) z[t] += __uint_as_float(r.w[t]);
+      break;
+    case 1:
+#pragma unroll
+      for (int t = 0; t < NV; ++t) {
+        const unsigned w = whole ? (t & 1 ? r.w[t / 2] & 0xFFFF0000u : r.w[t / 2] << 16) : r.w[t] << 16;
+        if (whole || col + t < N) z[t] += __uint_as_float(w);
+      }
+      break;
+    case 2:
+#pragma unroll
+      for (int t = 0; t < NV; ++t) {
+        const unsigned w = whole ? (t & 1 ? r.w[t / 2] >> 16 : r.w[t / 2]) : r.w[t];
+        if (whole || col + t < N) z[t] += half(w);
+      }
+      break;
+    default: break;
   }
 }
 
@@ -83,14 +118,14 @@ __device__ __forceinline__ void load_bias(const EpiArgs& e, int col, int N, floa
 }
 
 template <int NV>
-__device__ __forceinline__ void store_bf16(uint16_t* base, bool vec, int64_t row, int col, int N, const float (&f)[NV]) {
+__device__ __forceinline__ void store_bf16(uint16_t* base, int64_t row, int col, int N, const float (&f)[NV]) {
   uint16_t* dst = base + row * N + col;
   unsigned w[NV / 2];
 #pragma unroll
   for (int t = 0; t < NV / 2; ++t) w[t] = bf16_bits(f[2 * t]) | ((unsigned)bf16_bits(f[2 * t + 1]) << 16);
-  if (vec && col + NV <= N) {
-    if constexpr (NV == 8) *reinterpret_cast<v4u*>(dst) = (v4u){w[0], w[1], w[2], w[3]};
-    else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  if (col + NV <= N) {
+    if constexpr (NV == 8) *reinterpret_cast<v4u_at2*>(dst) = (v4u){w[0], w[1], w[2], w[3]};
+    else *reinterpret_cast<v2u_at2*>(dst) = (v2u_at2){w[0], w[1]};
   } else {
 #pragma unroll
     for (int t = 0; t < NV; ++t)
@@ -101,11 +136,11 @@ __device__ __forceinline__ void store_bf16(uint16_t* base, bool vec, int64_t row
 // pre and out of NV outputs from their products c, bias b and residual r.
 template <int NV>
 __device__ __forceinline__ void residual_store(const EpiArgs& e, int64_t row, int col, int N, const float (&c)[NV],
-                                               const float (&b)[NV], const float (&r)[NV]) {
+                                               const float (&b)[NV], const RawResidual<NV>& r) {
   float z[NV];
 #pragma unroll
   for (int t = 0; t < NV; ++t) z[t] = c[t] + b[t];
-  if (e.pre) store_bf16<NV>(e.pre, e.vec & 2, row, col, N, z);
+  if (e.pre) store_bf16<NV>(e.pre, row, col, N, z);
   switch (e.act) {  // the same for the whole launch
     case 1:
 #pragma unroll
@@ -125,34 +160,51 @@ __device__ __forceinline__ void residual_store(const EpiArgs& e, int64_t row, in
       break;
     default: break;
   }
-#pragma unroll
-  for (int t = 0; t < NV; ++t) z[t] += r[t];
-  store_bf16<NV>(e.out, e.vec & 1, row, col, N, z);
+  add_residual<NV>(e, col, N, r, z);
+  store_bf16<NV>(e.out, row, col, N, z);
 }
 
-// One pass of a tile's epilogue: the rows that are in LDS as FP32 (pitch LDF
-// floats, GR rows of each wave row's WTM, the pass's first at `first`), BN
-// columns from n0, by all NT threads. A thread's columns are the same in every
-// pass; bias: theirs.
-template <int BN, int LDF, int NT, int WM, int WTM, int GR>
-__device__ __forceinline__ void residual_pass(const EpiArgs& e, const float* tile, int m0, int n0, int first, int M, int N,
-                                              const float (&bias)[8]) {
-  constexpr int RPI = NT / (BN / 8), ITS = WM * GR / RPI;
-  static_assert(NT % (BN / 8) == 0 && (WM * GR) % RPI == 0, "rows split evenly over the threads");
-  const int c = (threadIdx.x % (BN / 8)) * 8, r0 = threadIdx.x / (BN / 8);
-  if (n0 + c >= N) return;
+// A tile's epilogue in passes: a pass is GR rows of each wave row's WTM rows
+// (the pass's first at `first`), BN columns from n0, in LDS as FP32 (pitch LDF
+// floats), stored by all NT threads, ITS rows each. A thread's columns are the
+// same in every pass.
+template <int BN_, int LDF_, int NT_, int WM_, int WTM_, int GR_>
+struct ResidualTile {
+  static constexpr int BN = BN_, LDF = LDF_, NT = NT_, WTM = WTM_, GR = GR_;
+  static constexpr int RPI = NT / (BN / 8), ITS = WM_ * GR / RPI;
+  static_assert(NT % (BN / 8) == 0 && (WM_ * GR) % RPI == 0, "rows split evenly over the threads");
+
+  const EpiArgs& e;
+  int m0, n0, M, N;
+
+  __device__ __forceinline__ int col() const { return (threadIdx.x % (BN / 8)) * 8; }
+  // the thread's row in LDS and in the output of iteration `it`
+  __device__ __forceinline__ int row(int it) const { return it * RPI + (int)threadIdx.x / (BN / 8); }
+  __device__ __forceinline__ int64_t out_row(int r, int first) const { return m0 + (r / GR) * WTM + first + r % GR; }
+
+  // The pass's residual: loaded a pass ahead, so that its latency passes
+  // behind the pass before it.
+  __device__ __forceinline__ void load(int first, RawResidual<8> (&res)[ITS]) const {
 #pragma unroll
-  for (int it = 0; it < ITS; ++it) {
-    const int r = it * RPI + r0;
-    const int64_t gr = m0 + (r / GR) * WTM + first + r % GR;
-    if (gr >= M) continue;
-    const v4f lo = *reinterpret_cast<const v4f*>(tile + r * LDF + c);
-    const v4f hi = *reinterpret_cast<const v4f*>(tile + r * LDF + c + 4);
-    const float p[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    float res[8];
-    load_residual<8>(e, gr, n0 + c, N, res);
-    residual_store<8>(e, gr, n0 + c, N, p, bias, res);
+    for (int it = 0; it < ITS; ++it) {
+      const int64_t gr = out_row(row(it), first);
+      if (gr < M && n0 + col() < N) load_residual<8>(e, gr, n0 + col(), N, res[it]);
+    }
   }
-}
+
+  __device__ __forceinline__ void store(const float* tile, int first, const float (&bias)[8], const RawResidual<8> (&res)[ITS]) const {
+    const int c = col();
+#pragma unroll
+    for (int it = 0; it < ITS; ++it) {
+      const int r = row(it);
+      const int64_t gr = out_row(r, first);
+      if (gr >= M || n0 + c >= N) continue;
+      const v4f lo = *reinterpret_cast<const v4f*>(tile + r * LDF + c);
+      const v4f hi = *reinterpret_cast<const v4f*>(tile + r * LDF + c + 4);
+      const float p[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      residual_store<8>(e, gr, n0 + c, N, p, bias, res[it]);
+    }
+  }
+};
 
 }  // namespace dg

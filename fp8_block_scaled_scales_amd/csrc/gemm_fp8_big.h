@@ -219,8 +219,16 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
     const int col = wc0 + (G == 128 ? j * 16 + (lane & 15) : j * 32 + (lane & 31));
     bj[j] = hb && col < N ? bias[col] : 0.0f;
   }
-  float b8[8];  // form 3: the columns this thread stores
-  if constexpr (EPI == 3) load_bias<8>(epi, n0 + (threadIdx.x % (BN / 8)) * 8, N, b8);
+
+  // Form 3: passes of 32 rows of every wave row. The first pass's residual is
+  // loaded ahead of the copies where its 32 registers are free during the main
+  // loop (the 256x128 tiles).
+  constexpr int GR = 32, LDF = BN + 4;
+  constexpr bool EARLY = BN == 128;
+  using Tile = ResidualTile<BN, LDF, NT, WM, WTM, GR>;
+  const Tile tile{epi, m0, n0, M, N};
+  RawResidual<8> res[2][Tile::ITS];
+  if constexpr (EPI == 3 && EARLY) tile.load(0, res[0]);
 
   issue_step(0);
 
@@ -387,9 +395,11 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
     // 32 rows of every wave row at a time, so that all waves write and all
     // threads store in every pass. The pitch puts rows four apart 16 banks
     // apart, where the 16x16 layout's lane groups write them.
-    constexpr int GR = 32, LDF = BN + 4;
     static_assert(WM * GR * LDF * 4 <= 2 * SLOT, "an epilogue pass must fit in the ring");
     float* const cf = reinterpret_cast<float*>(smem);
+    float b8[8];
+    if constexpr (!EARLY) tile.load(0, res[0]);
+    load_bias<8>(epi, n0 + tile.col(), N, b8);
 #pragma unroll
     for (int pass = 0; pass < WTM / GR; ++pass) {
       __syncthreads();
@@ -411,7 +421,8 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
             cf[(wm * GR + 8 * (v >> 2) + 4 * h2 + (v & 3)) * LDF + wn * WTN + j * 32 + r32] = acc.t[pass][j][v];
       }
       __syncthreads();
-      residual_pass<BN, LDF, NT, WM, WTM, GR>(epi, cf, m0, n0, pass * GR, M, N, b8);
+      if (pass + 1 < WTM / GR) tile.load((pass + 1) * GR, res[(pass + 1) & 1]);
+      tile.store(cf, pass * GR, b8, res[pass & 1]);
     }
     return;
   }

@@ -139,7 +139,8 @@ __global__ __launch_bounds__(64 * NW) void gemm_fp8_stream(const uint8_t* __rest
   // residual is that of the whole K loop.
   const int er = m0 + (int)(threadIdx.x >> 3), ec = n0 + 4 * (int)(threadIdx.x & 7);
   const bool e_live = er < M && ec < N;
-  float e_bias[4], e_res[4];
+  float e_bias[4];
+  RawResidual<4> e_res;
   if constexpr (EPI == 3) {
     if (e_live) {
       load_bias<4>(epi, ec, N, e_bias);

@@ -154,8 +154,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
     const int col = n0 + wn * WTN + j * 32 + (lane & 31);
     bcol[j] = hb && col < N ? bias[col] : 0.0f;
   }
-  float b8[8];  // form 3: the columns this thread stores
-  if constexpr (EPI == 3) load_bias<8>(epi, n0 + (threadIdx.x % (BN / 8)) * 8, N, b8);
+
+  // Form 3: the first pass's residual, ahead of the copies too.
+  using Tile = ResidualTile<BN, BN + 4, NT, WM, WTM, 32>;
+  const Tile tile{epi, m0, n0, M, N};
+  RawResidual<8> res[2][Tile::ITS];
+  if constexpr (EPI == 3) tile.load(0, res[0]);
 
   // Prologue: fill STAGES-1 ring slots.
 #pragma unroll
@@ -268,9 +272,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
 
   if constexpr (EPI == 3) {
     // one 32-row sub-tile of every wave row at a time
-    constexpr int LDF = BN + 4;
-    static_assert(WM * 32 * LDF * 4 <= STAGES * STAGE_BYTES, "an epilogue pass must fit in the ring");
+    static_assert(WM * 32 * Tile::LDF * 4 <= STAGES * STAGE_BYTES, "an epilogue pass must fit in the ring");
+    constexpr int LDF = Tile::LDF;
     float* const cf = reinterpret_cast<float*>(smem);
+    float b8[8];
+    load_bias<8>(epi, n0 + tile.col(), N, b8);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       __syncthreads();
@@ -280,7 +286,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
         for (int v = 0; v < 16; ++v)
           cf[(wm * 32 + (v >> 2) * 8 + half * 4 + (v & 3)) * LDF + wn * WTN + j * 32 + (lane & 31)] = acc[i][j][v];
       __syncthreads();
-      residual_pass<BN, LDF, NT, WM, WTM, 32>(epi, cf, m0, n0, i * 32, M, N, b8);
+      if (i + 1 < TM) tile.load((i + 1) * 32, res[(i + 1) & 1]);
+      tile.store(cf, i * 32, b8, res[i & 1]);
     }
     return;
   }
@@ -354,6 +361,31 @@ __global__ __launch_bounds__(256) void splitk_reduce(const float* __restrict__ w
   }
 }
 
+// The second kernel of a K split with a residual: the same sums, then
+// gemm_epilogue.h's epilogue. The residual is loaded ahead of the partials.
+template <int BM, int BN>
+__global__ __launch_bounds__(256) void splitk_reduce_residual(const float* __restrict__ ws, const EpiArgs epi, int M, int N,
+                                                              int tiles_n, int ksplit) {
+  constexpr int Q = BN / 4;
+  static_assert((BM * Q) % 256 == 0, "whole workgroups per tile");
+  const int tile = (int)(blockIdx.x / ((BM * Q) / 256));
+  const int e = (int)(blockIdx.x % ((BM * Q) / 256)) * 256 + (int)threadIdx.x;
+  const int r = e / Q, c = (e % Q) * 4;
+  const int gr = (tile / tiles_n) * BM + r, gc = (tile % tiles_n) * BN + c;
+  if (gr >= M || gc >= N) return;
+  float b[4], z[4];
+  RawResidual<4> res;
+  load_residual<4>(epi, gr, gc, N, res);
+  load_bias<4>(epi, gc, N, b);
+  const float* p = ws + (int64_t)tile * ksplit * (BM * BN) + r * BN + c;
+  v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int sp = 0; sp < ksplit; ++sp) sum += *reinterpret_cast<const v4f*>(p + (int64_t)sp * (BM * BN));
+#pragma unroll
+  for (int t = 0; t < 4; ++t) z[t] = sum[t];
+  residual_store<4>(epi, gr, gc, N, z, b, res);
+}
+
 // ---- launch table -------------------------------------------------------------
 
 template <int BM, int BN, int WM, int WN, int STAGES, int G, int GROUP_M, bool SPLIT, int FMT, int EPI, bool ROWA,
@@ -365,11 +397,15 @@ static hipError_t launch_tiled_fa(const GemmArgs& p, hipStream_t stream) {
                      (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.vec_store, p.ksplit, p.ws, p.sshift, p.bias,
                      p.act == 1 ? 1 : 0, p.epi);
   hipError_t err = hipGetLastError();
-  if constexpr (SPLIT && EPI != 3) {  // the form with a residual is planned without a split
+  if constexpr (SPLIT) {
     if (p.ksplit > 1 && err == hipSuccess) {
-      hipLaunchKernelGGL((splitk_reduce<BM, BN, EPI>), dim3(tiles_m * tiles_n * (BM * BN / 4 / 256)), dim3(256), 0,
-                         stream, p.ws, p.out, (int)p.M, (int)p.N, tiles_n, p.ksplit, p.vec_store, p.bias,
-                         p.act == 1 ? 1 : 0);
+      const dim3 grid(tiles_m * tiles_n * (BM * BN / 4 / 256));
+      if constexpr (EPI == 3)
+        hipLaunchKernelGGL((splitk_reduce_residual<BM, BN>), grid, dim3(256), 0, stream, p.ws, p.epi, (int)p.M, (int)p.N,
+                           tiles_n, p.ksplit);
+      else
+        hipLaunchKernelGGL((splitk_reduce<BM, BN, EPI>), grid, dim3(256), 0, stream, p.ws, p.out, (int)p.M, (int)p.N,
+                           tiles_n, p.ksplit, p.vec_store, p.bias, p.act == 1 ? 1 : 0);
       err = hipGetLastError();
     }
   }
@@ -416,7 +452,7 @@ static hipError_t launch_tiled_form(const GemmArgs& p, hipStream_t stream) {
 template <int BM, int BN, int WM, int WN, int STAGES, int G, int GROUP_M, bool SPLIT, int LAYOUT, int RS,
           bool RES = false>
 static hipError_t launch_tiled_l(const GemmArgs& p, hipStream_t stream) {
-  if (((!SPLIT || RES) && p.ksplit != 1) || p.sshift < 0 || p.sshift > 1) return hipErrorInvalidValue;
+  if ((!SPLIT && p.ksplit != 1) || p.sshift < 0 || p.sshift > 1) return hipErrorInvalidValue;
   switch (p.fmt) {
     case 0: return launch_tiled_form<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 0, LAYOUT, RS, RES>(p, stream);
     case 1: return launch_tiled_form<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 1, LAYOUT, RS, RES>(p, stream);

@@ -395,22 +395,29 @@ int dg_quantize_fp8_rows_typed(const void* x, int in_type, int64_t rows, int64_t
  * in FP32, each output rounded once.
  *
  *   a, b, sa, sb, out, M, N, K, gran, layout, sa_rows, fmt_a, fmt_b, bias
- *        as dg_gemm_fp8_ws without a workspace (the same tile choice).
+ *        as dg_gemm_fp8_ws.
  *   act  any of the five DG_ACT_* codes.
  *   res  [M][N] of res_type, row pitch ldres, aligned to its element, or NULL
  *        (res_type and ldres are then not read). It may be out itself (BF16,
  *        ldres = N): the stream is updated in place.
  *   pre  BF16 [M][N] out, 2-byte aligned, or NULL.
+ *   workspace, workspace_bytes  as dg_gemm_fp8_ws: with at least
+ *        dg_gemm_fp8_residual_workspace bytes, few output tiles and a long K
+ *        (from 8192, or from 6144 where an operand is stored transposed) split
+ *        K over workgroups; NULL and 0 for no split.
  *
- * Without res and pre and with one of the three activations of
- * dg_gemm_fp8_layout the result is that call's, bit for bit (with sa_rows = 1
- * dg_gemm_fp8_ws's). Accesses to out, pre and res are 16 bytes wide where
- * their bases and pitches allow it. Status codes as dg_gemm_fp8_layout.
+ * The product and pre are dg_gemm_fp8_ws's (without a workspace: its tile
+ * choice in every layout), and without res and pre and with one of its three
+ * activations the result is that call's, bit for bit. Status codes as dg_gemm_fp8_layout.
  */
 int dg_gemm_fp8_residual(const void* a, const void* b, const float* sa, const float* sb, void* out, int64_t M,
                          int64_t N, int64_t K, int gran, int layout, int sa_rows, int fmt_a, int fmt_b,
                          const float* bias, int act, const void* res, int res_type, int64_t ldres, void* pre,
-                         void* stream);
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes with which that call splits K for these sizes (0: it does
+ * not; DG_EINVAL for sizes it would reject). */
+int64_t dg_gemm_fp8_residual_workspace(int64_t M, int64_t N, int64_t K, int gran, int layout);
 
 /*
  * dg_rmsnorm_quantize_fp8 - the residual's addition, the root-mean-square norm

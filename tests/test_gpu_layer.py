@@ -313,6 +313,35 @@ def test_residual_in_place(dg, M, N, K):
     assert got is res and torch.equal(res, out)
 
 
+@pytest.mark.parametrize("M,N,K,g,layout", [(19, 51, 12352, 64, 3), (64, 512, 6144, 128, 1), (130, 68, 8192, 256, 2),
+                                            (64, 512, 16384, 128, 0), (1, 1, 16384, 64, 0)])
+def test_residual_with_a_split_k(dg, M, N, K, g, layout):
+    """Few tiles and a long K: pre is the split plain call's output to the bit, out is bf16(act(z) + residual), with the
+    workspace left to the call, given, and (without one) unsplit within the product's tolerance."""
+    need = dg.dg_gemm_fp8_residual_workspace(M, N, K, g, layout)
+    assert need > 0
+    a8, sa, b8, sb = _operands(M, N, K, g, rowa=True)
+    ta, tsa, tb, tsb = device_inputs(a8.T if layout & 2 else a8, sa, b8.T if layout & 1 else b8, sb)
+    kw = dict(gran=g, layout=layout, sa_rows=1, bias=torch.arange(N, device=DEV).float() / N)
+    res = ref.stream(N, M, N, F32)
+    say("residual split K %dx%dx%d layout %d" % (M, N, K, layout))
+    pre, pre2, out2 = (torch.empty(M, N, dtype=BF16, device=DEV) for _ in range(3))
+    out = dg.dg_gemm_fp8_residual(ta, tb, tsa, tsb, res=ref.padded(res, 3), pre=pre, act=1, **kw)
+    with _common.forced_split(g):
+        plain = dg.dg_gemm_fp8_ws(ta, tb, tsa, tsb, workspace=dg.dg_workspace(M, N, K, g, layout), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(pre.view(torch.int16), plain.view(torch.int16))
+    z = pre.cpu().double()
+    want = z.clamp(min=0) + res.double()
+    close(out, want, ref.half_step(BF16) * 1.02 * (z.abs() + want.abs()) + 1e-37, "out")
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    dg.dg_gemm_fp8_residual(ta, tb, tsa, tsb, res=ref.padded(res, 3), out=out2, pre=pre2, act=1, workspace=ws, **kw)
+    assert torch.equal(out2, out) and torch.equal(pre2, pre)
+    whole = oracle.gemm_ref_rowa(a8, b8, sa, sb, g) + (np.arange(N) / N)[None, :]
+    ok, _ = _common.within_tolerance(pre.float().cpu().numpy(), whole)
+    assert ok.all()
+
+
 def test_residual_race_check_build(dg):
     """The build with extra waits and barriers gives the same bits."""
     lib = dg.load_library(dg.SYNC_LIB_PATH)
@@ -323,7 +352,7 @@ def test_residual_race_check_build(dg):
         say("residual race check %dx%dx%d" % (M, N, K))
         want = dg.dg_gemm_fp8_residual(ta, tb, tsa, tsb, res=res, gran=g, act=4)
         rc = lib.dg_gemm_fp8_residual(ta.data_ptr(), tb.data_ptr(), tsa.data_ptr(), tsb.data_ptr(), out.data_ptr(), M, N, K, g, 0,
-                                      g, 0, 0, None, 4, res.data_ptr(), 1, N, pre.data_ptr(),
+                                      g, 0, 0, None, 4, res.data_ptr(), 1, N, pre.data_ptr(), None, 0,
                                       torch.cuda.current_stream().cuda_stream)
         torch.cuda.synchronize()
         assert rc == 0 and torch.equal(out, want)

@@ -87,9 +87,9 @@ def test_epilogue_backward_refuses(dg, kw, want):
 
 
 def _gemm(dg, a=X, b=W, sa=S, sb=RSTD, out=H, M=256, N=256, K=256, g=128, layout=0, sa_rows=128, fa=0, fb=0, bias=0, act=2,
-          res=RES, rk=1, ldres=256, pre=PRE):
+          res=RES, rk=1, ldres=256, pre=PRE, ws=0, nb=0):
     return dg.lib.dg_gemm_fp8_residual(a, b, sa, sb, out, M, N, K, g, layout, sa_rows, fa, fb, bias or None, act,
-                                       res or None, rk, ldres, pre or None, None)
+                                       res or None, rk, ldres, pre or None, ws or None, nb, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -100,6 +100,9 @@ def _gemm(dg, a=X, b=W, sa=S, sb=RSTD, out=H, M=256, N=256, K=256, g=128, layout
     (dict(bias=Q + 2), "EALIGN"), (dict(out=H + 1), "EALIGN"), (dict(a=X + 8), "EALIGN"),
     (dict(pre=H), "EINVAL"), (dict(pre=RES), "EINVAL"), (dict(pre=X), "EINVAL"), (dict(out=X), "EINVAL"),
     (dict(res=H, rk=0), "EINVAL"), (dict(res=H + 2), "EINVAL"), (dict(res=H, ldres=264), "EINVAL"),
+    (dict(ws=WS, nb=0), "EINVAL"), (dict(ws=0, nb=64), "EINVAL"), (dict(nb=-1), "EINVAL"), (dict(ws=WS + 16, nb=64), "EALIGN"),
+    (dict(ws=PRE, nb=64), "EINVAL"), (dict(ws=RES, nb=64), "EINVAL"), (dict(ws=H, nb=64), "EINVAL"),
+    (dict(M=64, N=64, K=32768, ldres=64, ws=WS, nb=64), "EINVAL"),  # less than the split needs
 ])
 def test_residual_product_refuses(dg, kw, want):
     assert _gemm(dg, **kw) == getattr(dg, "DG_" + want)
@@ -123,6 +126,14 @@ def test_workspace_sizes(dg):
     for bad in [(0, 64), (8, 100), (8, 0), (1 << 24, 64)]:
         with pytest.raises(ValueError):
             dg.dg_rmsnorm_backward_workspace(*bad)
+    # a K split: from 8192, with a transposed operand from 6144, and at least eight ways
+    for M, N, K, layout, splits in [(64, 512, 8064, 0, 0), (64, 512, 8192, 0, 16), (64, 512, 6144, 3, 12), (64, 512, 6016, 1, 0),
+                                    (64, 64, 8192, 2, 16), (64, 2176, 8192, 3, 8), (64, 2560, 8192, 3, 0), (4096, 4096, 8192, 3, 0)]:
+        tiles = -(-M // 64) * -(-N // 64)
+        assert dg.dg_gemm_fp8_residual_workspace(M, N, K, 128, layout) == 4 * 64 * 64 * tiles * splits, (M, N, K, layout)
+    for bad in [(0, 64, 128), (64, 64, 192)]:
+        with pytest.raises(ValueError):
+            dg.dg_gemm_fp8_residual_workspace(*bad)
     with pytest.raises(ValueError):
         dg.dg_epilogue_backward_workspace(8, 192, 128)
     with pytest.raises(ValueError):
