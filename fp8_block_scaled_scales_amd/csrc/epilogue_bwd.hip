@@ -27,29 +27,93 @@ namespace dg {
 namespace {
 
 // dz of eight elements (ACT 0: dout itself).
-template <int DK, int ACT, bool ONCE = false>
-__device__ __forceinline__ void grad8(const EpiBwdArgs& p, int64_t row, int64_t c, float (&z)[8]) {
-  widen8(load8<DK, ONCE>(p.dout, row * p.lddout + c), z);
+template <int DK, int ACT>
+__device__ __forceinline__ void grad8(const Raw8<DK>& dout, const Raw8<1>& pre, float (&z)[8]) {
+  widen8(dout, z);
   if constexpr (ACT != 0) {
-    float pre[8];
-    widen8(load8<1, ONCE>(p.pre, row * p.ldpre + c), pre);
+    float f[8];
+    widen8(pre, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] *= act_grad<ACT>(pre[i]);
+    for (int i = 0; i < 8; ++i) z[i] *= act_grad<ACT>(f[i]);
   }
 }
 
+template <int DK, int ACT, bool ONCE = false>
+__device__ __forceinline__ void grad8(const EpiBwdArgs& p, int64_t row, int64_t c, float (&z)[8]) {
+  const Raw8<DK> dout = load8<DK, ONCE>(p.dout, row * p.lddout + c);
+  Raw8<1> pre = {};
+  if constexpr (ACT != 0) pre = load8<1, ONCE>(p.pre, row * p.ldpre + c);
+  grad8<DK, ACT>(dout, pre, z);
+}
+
+// Where the launches are short, dbias without a second one: the first workgroups
+// of the grid take kFewCols columns each over all rows (four lanes of eight
+// columns, NT / 4 rows at a time) and compute dz once more, its inputs then
+// coming from L2. 64 columns would leave the arithmetic of 1091 x 768 on 12 CUs
+// (12.5 us; 8.0 at 32, 6.6 at 16), 16 columns read 32-byte pieces (328 x 3328
+// 5.9 us at 64, 5.1 at 32, 6.5 at 16).
+constexpr int kFewCols = 32;
+
+template <int DK, int ACT, int NT>
+__device__ __forceinline__ void few_rows_dbias(const EpiBwdArgs& p, int group) {
+  constexpr int CL = kFewCols / 8, RL = NT / CL;
+  __shared__ float red[RL][8 * CL];
+  const int rl = threadIdx.x / CL, c = (group * CL + threadIdx.x % CL) * 8;
+  float acc[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+  constexpr int U = 2;  // rows in flight per thread
+  for (int64_t r0 = rl; r0 < p.rows; r0 += U * RL) {
+    Raw8<DK> d[U];
+    Raw8<1> pre[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = r0 + u * RL < p.rows ? r0 + u * RL : r0;  // past the end: a row again, not counted
+      d[u] = load8<DK>(p.dout, r * p.lddout + c);
+      if (ACT != 0) pre[u] = load8<1>(p.pre, r * p.ldpre + c);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float z[8];
+      grad8<DK, ACT>(d[u], pre[u], z);
+      if (r0 + u * RL < p.rows) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += z[k];
+      }
+    }
+  }
+  column_sums_of_lanes<RL, CL>(acc, red, p.dbias + group * kFewCols);
+}
+
+// The same as a launch of its own, before the codes: dz written over dout would
+// change dout under the sums. NT as in the launch with the codes, so that the
+// order of the sums is that one's.
+template <int DK, int ACT, int NT>
+__global__ __launch_bounds__(NT) void epi_bwd_dbias(const EpiBwdArgs p) {
+  few_rows_dbias<DK, ACT, NT>(p, blockIdx.x);
+}
+
+// How a launch treats its data: FEW: dbias by few_rows_dbias in the same launch;
+// ONCE: nontemporal loads of the inputs and stores of the codes.
+enum Form { kPlain = 0, kFew = 1, kOnce = 2 };
+
 // One g x g block per workgroup of NT threads; dz in registers between the amax
-// and the encode. ONCE: nontemporal loads of the inputs and stores of the codes.
-template <int DK, int ACT, int G, int NT, bool ONCE>
-__global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* part) {
+// and the encode.
+template <int DK, int ACT, int G, int NT, int FORM>
+__global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* part, int col_wgs) {
+  constexpr bool ONCE = FORM == kOnce;
+  if constexpr (FORM == kFew) {
+    if ((int)blockIdx.x < col_wgs) return few_rows_dbias<DK, ACT, NT>(p, blockIdx.x);
+  }
+  const int block = blockIdx.x - (FORM == kFew ? col_wgs : 0);
   constexpr int ROW_L = G / 8;    // lanes per block row
   constexpr int RPP = NT / ROW_L;  // block rows covered by one pass
   constexpr int PASSES = G / RPP;
   static_assert(PASSES * RPP == G, "passes");
   __shared__ float red[NT / 64];
-  __shared__ float sums[RPP][G];
+  __shared__ float sums[FORM == kFew ? 1 : RPP][G];
   const int ncb = (int)(p.cols / G);
-  const int rb = blockIdx.x / ncb, cb = blockIdx.x % ncb;
+  const int rb = block / ncb, cb = block % ncb;
   const int t = threadIdx.x, rsub = t / ROW_L, cl = t % ROW_L;
   const int64_t c = (int64_t)cb * G + cl * 8;
 
@@ -69,7 +133,7 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
   }
   amax = group_max<64>(amax);
   if ((t & 63) == 0) red[t >> 6] = amax;
-  if (part) {
+  if (FORM != kFew && part) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) sums[rsub][cl * 8 + k] = acc[k];
   }
@@ -79,7 +143,7 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
   for (int w = 1; w < NT / 64; ++w) amax = fmaxf(amax, red[w]);
   const float s = block_scale(amax, format_max(p.fmt));
   const float inv = 1.0f / s;
-  if (t == 0) p.scales[blockIdx.x] = s;
+  if (t == 0) p.scales[block] = s;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int64_t r = (int64_t)rb * G + i * RPP + rsub;
@@ -90,7 +154,7 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
       if (p.dz) store8<DK>(p.dz, r * p.cols + c, round8<DK>(z[i]));
     }
   }
-  if (part && t < G) {
+  if (FORM != kFew && part && t < G) {
     float v = sums[0][t];
 #pragma unroll
     for (int i = 1; i < RPP; ++i) v += sums[i][t];
@@ -107,11 +171,16 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
 // at 16).
 constexpr int NW = 16;
 
-template <int DK, int ACT>
-__global__ __launch_bounds__(64 * NW) void epi_bwd_rows(const EpiBwdArgs p, float* part, int col_groups, int ranges) {
-  __shared__ float sums[NW][512];
+template <int DK, int ACT, int FORM>
+__global__ __launch_bounds__(64 * NW) void epi_bwd_rows(const EpiBwdArgs p, float* part, int col_groups, int ranges,
+                                                        int col_wgs) {
+  if constexpr (FORM == kFew) {
+    if ((int)blockIdx.x < col_wgs) return few_rows_dbias<DK, ACT, 64 * NW>(p, blockIdx.x);
+  }
+  const int block = blockIdx.x - (FORM == kFew ? col_wgs : 0);
+  __shared__ float sums[FORM == kFew ? 1 : NW][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cg = blockIdx.x % col_groups, rr = blockIdx.x / col_groups;
+  const int cg = block % col_groups, rr = block / col_groups;
   const int64_t c = (int64_t)cg * 512 + lane * 8;
   const int gshift = 31 - __builtin_clz(p.gran);
   const int64_t segs = p.cols >> gshift;
@@ -130,7 +199,7 @@ __global__ __launch_bounds__(64 * NW) void epi_bwd_rows(const EpiBwdArgs p, floa
       if (p.dz) store8<DK>(p.dz, r * p.cols + c, round8<DK>(z));
     }
   }
-  if (!part) return;
+  if (FORM == kFew || !part) return;
 #pragma unroll
   for (int k = 0; k < 8; ++k) sums[wave][lane * 8 + k] = acc[k];
   __syncthreads();
@@ -143,12 +212,26 @@ __global__ __launch_bounds__(64 * NW) void epi_bwd_rows(const EpiBwdArgs p, floa
   }
 }
 
-// Partial rows of dbias: one per row of blocks (g x g), or per workgroup of a
-// column group (1 x g): two workgroups per CU over all, a row per wave at least.
-int64_t partial_rows(int64_t rows, int64_t cols, int gran, int block_rows) {
-  if (block_rows != 1) return (rows + gran - 1) / gran;
+// Row ranges of the 1 x g form: two workgroups per CU over all, a row per wave at
+// least.
+int64_t row_ranges(int64_t rows, int64_t cols) {
   const int64_t r = 512 / ((cols + 511) / 512), most = (rows + NW - 1) / NW;
   return r < 1 ? 1 : r < most ? r : most;
+}
+
+// Rows and elements up to which dbias comes from the same launch (BF16, GELU or
+// its tanh form): 215 x 384 3.7 us against 6.4 in two launches, 328 x 3328 5.1
+// against 7.0, 1091 x 768 8.0 against 8.4, 218 x 13184 7.3 against 6.9, 1024 x
+// 4096 12.3 against 9.6.
+constexpr int64_t kFewRows = 1024, kFewElements = 3ll << 19;
+
+bool few_rows(int64_t rows, int64_t cols) { return rows <= kFewRows && rows * cols <= kFewElements; }
+
+// Partial rows of dbias (one: the sums go straight to it): a row of blocks each
+// (g x g), or a row range each (1 x g).
+int64_t partial_rows(int64_t rows, int64_t cols, int gran, int block_rows) {
+  const int64_t n = block_rows == 1 ? row_ranges(rows, cols) : (rows + gran - 1) / gran;
+  return few_rows(rows, cols) ? 1 : n;
 }
 
 // Inputs of 64 MB and more (twice the L2s) are loaded, and their codes stored,
@@ -160,9 +243,15 @@ template <int DK, int ACT, int G, int NT>
 void launch_blocks(const EpiBwdArgs& p, float* part, hipStream_t stream) {
   const dim3 grid((unsigned)(((p.rows + G - 1) / G) * (p.cols / G)));
   if (p.rows * p.cols * (InKind<DK>::kBytes + (ACT ? 2 : 0)) >= kOnceBytes)
-    hipLaunchKernelGGL((epi_bwd_blocks<DK, ACT, G, NT, true>), grid, dim3(NT), 0, stream, p, part);
+    hipLaunchKernelGGL((epi_bwd_blocks<DK, ACT, G, NT, kOnce>), grid, dim3(NT), 0, stream, p, part, 0);
   else
-    hipLaunchKernelGGL((epi_bwd_blocks<DK, ACT, G, NT, false>), grid, dim3(NT), 0, stream, p, part);
+    hipLaunchKernelGGL((epi_bwd_blocks<DK, ACT, G, NT, kPlain>), grid, dim3(NT), 0, stream, p, part, 0);
+}
+
+template <int DK, int ACT, int G, int NT>
+void launch_blocks_few(const EpiBwdArgs& p, int col_wgs, hipStream_t stream) {
+  const dim3 grid((unsigned)(((p.rows + G - 1) / G) * (p.cols / G) + col_wgs));
+  hipLaunchKernelGGL((epi_bwd_blocks<DK, ACT, G, NT, kFew>), grid, dim3(NT), 0, stream, p, nullptr, col_wgs);
 }
 
 // Threads per block. At g = 128 512 (four pieces of eight elements per thread)
@@ -175,18 +264,38 @@ void launch_blocks(const EpiBwdArgs& p, float* part, hipStream_t stream) {
 template <int DK, int ACT>
 hipError_t launch_act(const EpiBwdArgs& p, hipStream_t stream) {
   const int64_t n = partial_rows(p.rows, p.cols, p.gran, p.block_rows);
-  float* const part = !p.dbias ? nullptr : n > 1 ? p.ws : p.dbias;
+  float* part = !p.dbias ? nullptr : n > 1 ? p.ws : p.dbias;
+  // one row of blocks (or one range) has dbias' sums already
+  const int64_t ranges = row_ranges(p.rows, p.cols);
+  bool few = p.dbias && few_rows(p.rows, p.cols) && (p.block_rows == 1 ? ranges > 1 : p.rows > p.gran);
+  if (few && p.dz == p.dout) {
+    const dim3 grid((unsigned)(p.cols / kFewCols));
+    if (p.block_rows == 64) hipLaunchKernelGGL((epi_bwd_dbias<DK, ACT, 512>), grid, dim3(512), 0, stream, p);
+    else hipLaunchKernelGGL((epi_bwd_dbias<DK, ACT, 1024>), grid, dim3(1024), 0, stream, p);
+    few = false;
+    part = nullptr;
+  }
+  const int col_wgs = few ? (int)(p.cols / kFewCols) : 0;
+  const int64_t blocks = ((p.rows + p.gran - 1) / p.gran) * (p.cols / p.gran);
   if (p.block_rows == 1) {
     const int64_t col_groups = (p.cols + 511) / 512;
-    hipLaunchKernelGGL((epi_bwd_rows<DK, ACT>), dim3((unsigned)(col_groups * n)), dim3(64 * NW), 0, stream, p, part,
-                       (int)col_groups, (int)n);
+    const dim3 grid((unsigned)(col_groups * ranges + col_wgs));
+    if (few)
+      hipLaunchKernelGGL((epi_bwd_rows<DK, ACT, kFew>), grid, dim3(64 * NW), 0, stream, p, nullptr, (int)col_groups,
+                         (int)ranges, col_wgs);
+    else
+      hipLaunchKernelGGL((epi_bwd_rows<DK, ACT, kPlain>), grid, dim3(64 * NW), 0, stream, p, part, (int)col_groups,
+                         (int)ranges, 0);
   } else if (p.gran == 64) {
-    launch_blocks<DK, ACT, 64, 256>(p, part, stream);
+    if (few) launch_blocks_few<DK, ACT, 64, 512>(p, col_wgs, stream);
+    else launch_blocks<DK, ACT, 64, 256>(p, part, stream);
   } else if (p.gran == 128) {
-    if (DK == 0 || ((p.rows + 127) / 128) * (p.cols / 128) <= 1024) launch_blocks<DK, ACT, 128, 1024>(p, part, stream);
+    if (few) launch_blocks_few<DK, ACT, 128, 1024>(p, col_wgs, stream);
+    else if (DK == 0 || blocks <= 1024) launch_blocks<DK, ACT, 128, 1024>(p, part, stream);
     else launch_blocks<DK, ACT, 128, 512>(p, part, stream);
   } else {
-    launch_blocks<DK, ACT, 256, 1024>(p, part, stream);
+    if (few) launch_blocks_few<DK, ACT, 256, 1024>(p, col_wgs, stream);
+    else launch_blocks<DK, ACT, 256, 1024>(p, part, stream);
   }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || !p.dbias || n == 1) return err;

@@ -34,13 +34,13 @@ namespace dg {
 namespace {
 
 // Sum over the RT threads that share a row, in every one of them: RT = 64 is
-// one wave; else the workgroup's waves meet through LDS (red: RT / 64 floats,
-// free again after the next barrier), added in wave order.
+// one wave; else the waves meet through LDS (red: RT / 64 floats of the row's
+// own, free again after the workgroup's next barrier), added in wave order. t:
+// the thread's place in its row.
 template <int RT>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+__device__ __forceinline__ float row_sum(float v, float* red, int t) {
   v = wave_sum(v);
   if constexpr (RT > 64) {
-    const int t = threadIdx.x;
     if ((t & 63) == 0) red[t >> 6] = v;
     __syncthreads();
     v = red[0];
@@ -100,11 +100,11 @@ template <int XK, int RK, int RT, int C>
 __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_quant(const NormArgs p) {
   constexpr int HK = RK == kAbsent ? XK : RK;
   constexpr int ROWS = RT < 256 ? 256 / RT : 1;
-  __shared__ float red[RT / 64];
-  const int t = threadIdx.x % RT;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / RT;
-  if (row >= p.rows) return;  // RT = 64 only: whole waves, and no barrier follows
-  const int chunks = (int)(p.cols / 8);
+  __shared__ float red[ROWS][RT / 64];
+  const int t = threadIdx.x % RT, team = threadIdx.x / RT;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + team;
+  if (RT == 64 && row >= p.rows) return;  // whole waves, and no barrier follows
+  const int chunks = row < p.rows ? (int)(p.cols / 8) : 0;  // a team past the last row only meets the barrier
   Raw8<HK> h[C];
   float ss = 0.0f;
 #pragma unroll
@@ -120,9 +120,9 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_quant(const NormA
       if (RK != kAbsent) store8<HK>(p.h, row * p.cols + 8 * ch, h[i]);
     }
   }
-  ss = row_sum<RT>(ss, red);
+  ss = row_sum<RT>(ss, red[team], t);
   const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
-  if (p.rstd && t == 0) p.rstd[row] = rstd;
+  if (p.rstd && t == 0 && chunks) p.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int ch = i * RT + t;
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long(const NormArgs p) {
     ss += sum_sq8(h);
     if (RK != kAbsent) store8<HK>(p.h, row * p.cols + 8 * ch, h);
   }
-  ss = row_sum<RT>(ss, red);
+  ss = row_sum<RT>(ss, red, t);
   const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
   if (p.rstd && t == 0) p.rstd[row] = rstd;
   for (int ch = t; ch < chunks; ch += RT) {
@@ -169,10 +169,17 @@ hipError_t launch_rows(const NormArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Threads per row: one chunk each as long as 1024 reach, which leaves the
+// fewest bytes waiting at each row's barrier and gives a single row the most
+// lanes. Two or four chunks per thread: 8192x2048 23.2 -> 25.6 and 30.2 us,
+// 8192x8192 (training) 105 -> 110 and 120, one row of 7168 3.2 -> 3.6 and 4.8;
+// half of the lanes idle: 4096x4096 24.2 -> 30.0, 8192x1024 12.1 -> 13.3.
 template <int XK, int RK>
 hipError_t launch_norm_k(const NormArgs& p, hipStream_t stream) {
   if (p.cols <= 512) return launch_rows<XK, RK, 64, 1>(p, stream);
+  if (p.cols <= 1024) return launch_rows<XK, RK, 128, 1>(p, stream);
   if (p.cols <= 2048) return launch_rows<XK, RK, 256, 1>(p, stream);
+  if (p.cols <= 4096) return launch_rows<XK, RK, 512, 1>(p, stream);
   if (p.cols <= 8192) return launch_rows<XK, RK, 1024, 1>(p, stream);
   if (p.cols <= 16384) return launch_rows<XK, RK, 1024, 2>(p, stream);
   if (p.cols <= 32768) return launch_rows<XK, RK, 1024, 4>(p, stream);
@@ -224,16 +231,15 @@ __device__ __forceinline__ Raw8<HK> load_dh8(const NormBwdArgs& p, int64_t row, 
 }
 
 // Few rows, one launch and no workspace: the first `col_wgs` workgroups add
-// dy * n over all rows, 64 columns each (eight lanes of eight columns, their
-// sums over the threads' rows added through LDS in a fixed order); the others
-// take a row per RT threads. dy and h are read twice, from L2 the second time.
+// dy * n over all rows, 64 columns each (eight lanes of eight columns, 128 rows
+// at a time, their sums added through LDS in a fixed order); the others take a
+// row per RT threads. dy and h are read twice, the second time from L2.
 template <int DK, int HK, int RT, int C>
-__global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_few(const NormBwdArgs p, int col_wgs) {
-  constexpr int NT = RT < 256 ? 256 : RT, ROWS = NT / RT, RL = NT / 8;
-  __shared__ float red[RL][64];
+__global__ __launch_bounds__(1024) void rmsnorm_bwd_few(const NormBwdArgs p, int col_wgs) {
+  constexpr int NT = 1024, ROWS = NT / RT, CL = 8, RL = NT / CL;
+  __shared__ float red[RL][8 * CL];
   if ((int)blockIdx.x < col_wgs) {
-    const int cl = threadIdx.x % 8, rl = threadIdx.x / 8;
-    const int c = blockIdx.x * 64 + cl * 8;
+    const int rl = threadIdx.x / CL, c = (blockIdx.x * CL + threadIdx.x % CL) * 8;
     float acc[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
@@ -246,22 +252,13 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_few(const Nor
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(g[k], h[k] * rstd, acc[k]);
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) red[rl][cl * 8 + k] = acc[k];
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      float v = red[0][threadIdx.x];
-#pragma unroll
-      for (int i = 1; i < RL; ++i) v += red[i][threadIdx.x];
-      p.dw[blockIdx.x * 64 + threadIdx.x] = v;
-    }
+    column_sums_of_lanes<RL, CL>(acc, red, p.dw + blockIdx.x * (8 * CL));
     return;
   }
-  const int t = threadIdx.x % RT;
-  const int64_t row = (int64_t)(blockIdx.x - col_wgs) * ROWS + threadIdx.x / RT;
-  if (row >= p.rows) return;  // RT = 64 only: whole waves, and no barrier follows
-  const int chunks = (int)(p.cols / 8);
-  const float rstd = p.rstd[row];
+  const int t = threadIdx.x % RT, team = threadIdx.x / RT;
+  const int64_t row = (int64_t)(blockIdx.x - col_wgs) * ROWS + team;
+  const int chunks = row < p.rows ? (int)(p.cols / 8) : 0;  // a team past the last row only meets the barrier
+  const float rstd = chunks ? p.rstd[row] : 0.0f;
   Raw8<DK> dy[C];
   Raw8<HK> h[C], dh[C];
   float w[C][8], s = 0.0f;
@@ -278,7 +275,7 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_few(const Nor
 #pragma unroll
   for (int i = 0; i < C; ++i)
     if (i * RT + t < chunks) s += row_part8<DK, HK>(dy[i], h[i], w[i], rstd);
-  s = row_sum<RT>(s, &red[0][0]) / (float)p.cols;
+  s = row_sum<RT>(s, &red[0][0] + team * (RT / 64), t) / (float)p.cols;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int ch = i * RT + t;
@@ -355,7 +352,7 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
     const bool more = row + teams < p.rows;
     if (more) load_row(row + teams, dy1, h1, dh1, rstd1);
     // two areas in turn: a wave writes one again only after the other's barrier
-    s = row_sum<RT>(s, red[it & 1]) / (float)p.cols;
+    s = row_sum<RT>(s, red[it & 1], t) / (float)p.cols;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int ch = i * RT + t;
@@ -412,7 +409,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_rows_long(const NormBwdArgs 
     load_w8(p.w, 8 * ch, w);
     s += row_part8<DK, HK>(load8<DK>(p.dy, row * p.lddy + 8 * ch), load8<HK>(p.h, row * p.ldh + 8 * ch), w, rstd);
   }
-  s = row_sum<RT>(s, red) / (float)p.cols;
+  s = row_sum<RT>(s, red, (int)threadIdx.x) / (float)p.cols;
   for (int ch = threadIdx.x; ch < chunks; ch += RT) {
     float w[8];
     load_w8(p.w, 8 * ch, w);
@@ -455,7 +452,17 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_cols(const NormBwdArgs p, flo
 
 // The backward pass's form and its number of partial rows of dw.
 constexpr int64_t kLongCols = 16384;  // what rmsnorm_bwd_many holds
-constexpr int64_t kFewRows = 128;
+// Few rows: up to 2048 of them and 6M elements (dy and h then stay in the L2s
+// between their two readings) rmsnorm_bwd_few's one launch beats two: 139x1216
+// 2.9 us against 6.0, 512x4096 6.7 against 9.8, 1024x2048 7.6 against 10.0;
+// 2000x2048 13.3 against 13.2, 1024x8192 17.8 against 17.4, 1024x16384 39.6
+// against 33.6 (BF16; two launches with kTeamRows).
+constexpr int64_t kFewRows = 2048, kFewElements = 6ll << 20;
+
+// Rows that a team takes at least, so that the partial rows stay few beside the
+// rows: 2000x2048 15.5 us at one, 13.2 at four, 12.6 at eight; 3022x768 11.9,
+// 11.4 and 12.8.
+constexpr int64_t kTeamRows = 4;
 
 struct BwdPlan {
   bool few;
@@ -466,13 +473,13 @@ struct BwdPlan {
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
   BwdPlan b;
   b.rt = cols <= 512 ? 64 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
-  b.few = cols <= kLongCols && rows <= kFewRows;
+  b.few = cols <= kLongCols && rows <= kFewRows && rows * cols <= kFewElements;
   if (b.few) {
     b.partial = 1;
   } else if (cols <= kLongCols) {
     // 1024 threads per CU
     const int64_t wg_rows = b.rt < 256 ? 256 / b.rt : 1, wgs = 256 * (1024 / (b.rt < 256 ? 256 : b.rt));
-    b.partial = std::min<int64_t>((rows + wg_rows - 1) / wg_rows, wgs);
+    b.partial = std::min<int64_t>((rows + wg_rows * kTeamRows - 1) / (wg_rows * kTeamRows), wgs);
   } else {
     // about 1024 workgroups of rmsnorm_bwd_cols, at least 16 rows each
     b.partial = std::max<int64_t>(1, std::min<int64_t>(1024 / ((cols + 511) / 512), (rows + 15) / 16));
@@ -482,13 +489,13 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
 
 template <int DK, int HK, int RT, int C>
 void launch_bwd(const NormBwdArgs& p, const BwdPlan& b, hipStream_t stream) {
-  constexpr int NT = RT < 256 ? 256 : RT, ROWS = NT / RT;
   if (b.few) {
+    constexpr int ROWS = 1024 / RT;
     const int col_wgs = (int)(p.cols / 64);
-    hipLaunchKernelGGL((rmsnorm_bwd_few<DK, HK, RT, C>), dim3((unsigned)(col_wgs + (p.rows + ROWS - 1) / ROWS)), dim3(NT), 0,
+    hipLaunchKernelGGL((rmsnorm_bwd_few<DK, HK, RT, C>), dim3((unsigned)(col_wgs + (p.rows + ROWS - 1) / ROWS)), dim3(1024), 0,
                        stream, p, col_wgs);
   } else {
-    hipLaunchKernelGGL((rmsnorm_bwd_many<DK, HK, RT, C>), dim3((unsigned)b.partial), dim3(NT), 0, stream, p);
+    hipLaunchKernelGGL((rmsnorm_bwd_many<DK, HK, RT, C>), dim3((unsigned)b.partial), dim3(RT < 256 ? 256 : RT), 0, stream, p);
   }
 }
 

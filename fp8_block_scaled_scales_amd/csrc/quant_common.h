@@ -251,4 +251,27 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// A workgroup of RL x CL threads whose thread (rl, cl) holds partial sums of
+// columns 8 cl .. 8 cl + 7 of 8 CL: their totals to out, in a fixed order (every
+// group of 8 CL threads adds eight rows, then the first adds the groups).
+template <int RL, int CL>
+__device__ __forceinline__ void column_sums_of_lanes(const float (&acc)[8], float (&red)[RL][8 * CL], float* out) {
+  const int cl = threadIdx.x % CL, rl = threadIdx.x / CL;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) red[rl][cl * 8 + k] = acc[k];
+  __syncthreads();
+  const int c = threadIdx.x % (8 * CL), g = threadIdx.x / (8 * CL);
+  float v = red[g * 8][c];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v += red[g * 8 + i][c];
+  __syncthreads();
+  red[g][c] = v;
+  __syncthreads();
+  if (g == 0) {
+#pragma unroll 16
+    for (int i = 1; i < RL / 8; ++i) v += red[i][c];
+    out[c] = v;
+  }
+}
+
 }  // namespace dg

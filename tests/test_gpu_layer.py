@@ -99,7 +99,10 @@ def test_norm_of_zeros_and_extremes(dg):
 @pytest.mark.parametrize("dk,hk,with_dh,pad", [(BF16, BF16, True, 0), (BF16, F32, True, 8), (F16, F16, False, 8),
                                                (F32, F32, True, 0), (F32, BF16, True, 64), (F16, F32, False, 0)])
 @pytest.mark.parametrize("rows,cols", [(1, 64), (1, 8192), (3, 192), (64, 7168), (130, 512), (257, 2048), (19, 8256),
-                                       (300, 4096), (40, 16384), (5, 32768), (3, 65536), (1000, 64)])
+                                       (300, 4096), (40, 16384), (5, 32768), (3, 65536), (1000, 64),
+                                       # two launches, for every number of threads per row
+                                       (2100, 64), (2100, 512), (2600, 768), (3200, 2048), (1700, 4096), (900, 8192),
+                                       (420, 16384), (1030, 6208)])
 def test_norm_backward(dg, rows, cols, dk, hk, with_dh, pad):
     h, dy = ref.stream(rows, rows, cols, hk), ref.stream(cols, rows, cols, dk)
     dh = ref.stream(rows + cols, rows, cols, hk) if with_dh else None
@@ -159,7 +162,10 @@ ACT_ABS = 4e-7
     (1, 64, 64, False, BF16, 0, 1), (1, 64, 64, True, F32, 0, 1), (64, 4096, 128, False, BF16, 0, 1),
     (129, 256, 128, False, F32, 8, 0), (300, 512, 256, False, BF16, 8, 1), (65, 192, 64, False, F16, 0, 0),
     (2000, 576, 64, True, BF16, 64, 1), (37, 1280, 256, True, F16, 8, 0), (5, 128, 128, True, F32, 0, 1),
-    (513, 1024, 128, False, F16, 0, 1), (700, 640, 64, False, BF16, 0, 0)])
+    (513, 1024, 128, False, F16, 0, 1), (700, 640, 64, False, BF16, 0, 0),
+    # dbias in a second launch; the last by 512 threads per block, nontemporally
+    (1100, 640, 64, False, F16, 8, 1), (1500, 1152, 128, False, BF16, 0, 0), (1300, 1280, 256, False, F32, 0, 1),
+    (300, 640, 128, True, BF16, 0, 1), (1030, 1600, 64, True, F32, 4 * 2, 0), (4200, 4096, 128, False, BF16, 0, 1)])
 def test_epilogue_backward(dg, act, rows, cols, g, by_rows, dk, pad, fmt):
     dout = ref.stream(rows + cols, rows, cols, dk, zero_rows=(3,)) * 0.01
     pre = (torch.randn(rows, cols, generator=torch.Generator().manual_seed(rows)) * 2).to(BF16)
@@ -497,9 +503,9 @@ def test_short_way_refuses_the_same(dg):
     with pytest.raises(dg.DGArgumentError):  # a row pitch that is no multiple of 16 bytes
         wide = torch.ones(4, 257, dtype=BF16, device=DEV)
         dg.dg_rmsnorm_quantize_fp8(wide[:, :256], x, w, 1e-6, h=h, q=q, scales=s)
-    many = torch.ones(1000, 256, dtype=BF16, device=DEV)
+    many = torch.ones(5000, 256, dtype=BF16, device=DEV)
     with pytest.raises(dg.DGArgumentError):  # a workspace that is too small
-        dg.dg_rmsnorm_backward(many, many, torch.ones(1000, device=DEV), w, dx=torch.empty_like(many),
+        dg.dg_rmsnorm_backward(many, many, torch.ones(5000, device=DEV), w, dx=torch.empty_like(many),
                                dweight=torch.empty_like(w), workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
 
 

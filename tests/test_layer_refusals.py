@@ -76,11 +76,11 @@ def _epi(dg, dout=X, dk=1, lddout=256, pre=PRE, ldpre=256, act=2, rows=300, cols
     (dict(act=0), "EINVAL"), (dict(act=5), "EINVAL"), (dict(act=-1), "EINVAL"), (dict(dk=3), "EINVAL"),
     (dict(fmt=2), "EINVAL"), (dict(rows=0), "EINVAL"), (dict(cols=192), "EINVAL"), (dict(g=96, br=96), "EINVAL"),
     (dict(br=64), "EINVAL"), (dict(br=0), "EINVAL"), (dict(lddout=255), "EINVAL"), (dict(ldpre=0), "EINVAL"),
-    (dict(ws=0, nb=0), "EINVAL"), (dict(nb=16), "EINVAL"), (dict(nb=-1, db=0), "EINVAL"),
+    (dict(rows=4096, ws=0, nb=0), "EINVAL"), (dict(rows=4096, nb=16), "EINVAL"), (dict(nb=-1, db=0), "EINVAL"),
     (dict(dout=X + 8), "EALIGN"), (dict(lddout=257), "EALIGN"), (dict(ldpre=260), "EALIGN"), (dict(dz=Y + 8), "EALIGN"),
     (dict(q=Q + 4), "EALIGN"), (dict(db=DW + 2), "EALIGN"), (dict(s=S + 2), "EALIGN"), (dict(ws=WS + 4), "EALIGN"),
     (dict(dz=PRE), "EINVAL"), (dict(q=X), "EINVAL"), (dict(db=PRE), "EINVAL"), (dict(dz=X, lddout=512), "EINVAL"),
-    (dict(ws=X), "EINVAL"), (dict(s=Q), "EINVAL"),
+    (dict(rows=4096, ws=X), "EINVAL"), (dict(s=Q), "EINVAL"),
 ])
 def test_epilogue_backward_refuses(dg, kw, want):
     assert _epi(dg, **kw) == getattr(dg, "DG_" + want)
