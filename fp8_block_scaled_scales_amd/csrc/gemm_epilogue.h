@@ -46,8 +46,15 @@ struct RawResidual {
   unsigned w[NV];
 };
 
-// From (row, col) on; row < M and col < N.
-template <int NV>
+template <bool ONCE, class V>
+__device__ __forceinline__ V load_wide(const V* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+
+// From (row, col) on; row < M and col < N. ONCE (here and below): nontemporal
+// 16-byte accesses.
+template <int NV, bool ONCE = false>
 __device__ __forceinline__ void load_residual(const EpiArgs& e, int64_t row, int col, int N, RawResidual<NV>& r) {
   if (e.res_kind == 3) return;
   const int64_t at = row * e.ldres + col;
@@ -56,14 +63,14 @@ __device__ __forceinline__ void load_residual(const EpiArgs& e, int64_t row, int
       const float* src = static_cast<const float*>(e.res) + at;
 #pragma unroll
       for (int q = 0; q < NV / 4; ++q) {
-        const v4f v = *reinterpret_cast<const v4f_at4*>(src + 4 * q);
+        const v4f v = load_wide<ONCE>(reinterpret_cast<const v4f_at4*>(src + 4 * q));
 #pragma unroll
         for (int t = 0; t < 4; ++t) r.w[4 * q + t] = __float_as_uint(v[t]);
       }
     } else {
       const uint16_t* src = static_cast<const uint16_t*>(e.res) + at;
       if constexpr (NV == 8) {
-        const v4u v = *reinterpret_cast<const v4u_at2*>(src);
+        const v4u v = load_wide<ONCE>(reinterpret_cast<const v4u_at2*>(src));
 #pragma unroll
         for (int t = 0; t < 4; ++t) r.w[t] = v[t];
       } else {
@@ -117,14 +124,16 @@ __device__ __forceinline__ void load_bias(const EpiArgs& e, int col, int N, floa
   for (int t = 0; t < NV; ++t) b[t] = e.bias && col + t < N ? e.bias[col + t] : 0.0f;
 }
 
-template <int NV>
+template <int NV, bool ONCE>
 __device__ __forceinline__ void store_bf16(uint16_t* base, int64_t row, int col, int N, const float (&f)[NV]) {
   uint16_t* dst = base + row * N + col;
   unsigned w[NV / 2];
 #pragma unroll
   for (int t = 0; t < NV / 2; ++t) w[t] = bf16_bits(f[2 * t]) | ((unsigned)bf16_bits(f[2 * t + 1]) << 16);
   if (col + NV <= N) {
-    if constexpr (NV == 8) *reinterpret_cast<v4u_at2*>(dst) = (v4u){w[0], w[1], w[2], w[3]};
+    if constexpr (NV == 8 && ONCE)
+      __builtin_nontemporal_store((v4u_at2){w[0], w[1], w[2], w[3]}, reinterpret_cast<v4u_at2*>(dst));
+    else if constexpr (NV == 8) *reinterpret_cast<v4u_at2*>(dst) = (v4u){w[0], w[1], w[2], w[3]};
     else *reinterpret_cast<v2u_at2*>(dst) = (v2u_at2){w[0], w[1]};
   } else {
 #pragma unroll
@@ -134,13 +143,13 @@ __device__ __forceinline__ void store_bf16(uint16_t* base, int64_t row, int col,
 }
 
 // pre and out of NV outputs from their products c, bias b and residual r.
-template <int NV>
+template <int NV, bool ONCE = false>
 __device__ __forceinline__ void residual_store(const EpiArgs& e, int64_t row, int col, int N, const float (&c)[NV],
                                                const float (&b)[NV], const RawResidual<NV>& r) {
   float z[NV];
 #pragma unroll
   for (int t = 0; t < NV; ++t) z[t] = c[t] + b[t];
-  if (e.pre) store_bf16<NV>(e.pre, row, col, N, z);
+  if (e.pre) store_bf16<NV, ONCE>(e.pre, row, col, N, z);
   switch (e.act) {  // the same for the whole launch
     case 1:
 #pragma unroll
@@ -161,14 +170,14 @@ __device__ __forceinline__ void residual_store(const EpiArgs& e, int64_t row, in
     default: break;
   }
   add_residual<NV>(e, col, N, r, z);
-  store_bf16<NV>(e.out, row, col, N, z);
+  store_bf16<NV, ONCE>(e.out, row, col, N, z);
 }
 
 // A tile's epilogue in passes: a pass is GR rows of each wave row's WTM rows
 // (the pass's first at `first`), BN columns from n0, in LDS as FP32 (pitch LDF
 // floats), stored by all NT threads, ITS rows each. A thread's columns are the
 // same in every pass.
-template <int BN_, int LDF_, int NT_, int WM_, int WTM_, int GR_>
+template <int BN_, int LDF_, int NT_, int WM_, int WTM_, int GR_, bool ONCE = false>
 struct ResidualTile {
   static constexpr int BN = BN_, LDF = LDF_, NT = NT_, WTM = WTM_, GR = GR_;
   static constexpr int RPI = NT / (BN / 8), ITS = WM_ * GR / RPI;
@@ -188,7 +197,7 @@ struct ResidualTile {
 #pragma unroll
     for (int it = 0; it < ITS; ++it) {
       const int64_t gr = out_row(row(it), first);
-      if (gr < M && n0 + col() < N) load_residual<8>(e, gr, n0 + col(), N, res[it]);
+      if (gr < M && n0 + col() < N) load_residual<8, ONCE>(e, gr, n0 + col(), N, res[it]);
     }
   }
 
@@ -202,7 +211,7 @@ struct ResidualTile {
       const v4f lo = *reinterpret_cast<const v4f*>(tile + r * LDF + c);
       const v4f hi = *reinterpret_cast<const v4f*>(tile + r * LDF + c + 4);
       const float p[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      residual_store<8>(e, gr, n0 + c, N, p, bias, res[it]);
+      residual_store<8, ONCE>(e, gr, n0 + c, N, p, bias, res[it]);
     }
   }
 };

@@ -222,10 +222,12 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
 
   // Form 3: passes of 32 rows of every wave row. The first pass's residual is
   // loaded ahead of the copies where its 32 registers are free during the main
-  // loop (the 256x128 tiles).
+  // loop (the 256x128 tiles). The outputs of these tiles pass the caches by, as
+  // the residual does, and leave them to the operands: 8192^3 with BF16 residual
+  // and pre 500.6 -> 481.9 us (with bias and GELU 519.0 -> 505.6).
   constexpr int GR = 32, LDF = BN + 4;
   constexpr bool EARLY = BN == 128;
-  using Tile = ResidualTile<BN, LDF, NT, WM, WTM, GR>;
+  using Tile = ResidualTile<BN, LDF, NT, WM, WTM, GR, true>;
   const Tile tile{epi, m0, n0, M, N};
   RawResidual<8> res[2][Tile::ITS];
   if constexpr (EPI == 3 && EARLY) tile.load(0, res[0]);
