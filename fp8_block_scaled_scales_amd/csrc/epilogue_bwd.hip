@@ -148,9 +148,7 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
   for (int i = 0; i < PASSES; ++i) {
     const int64_t r = (int64_t)rb * G + i * RPP + rsub;
     if (r < p.rows) {
-      v2i* const q = reinterpret_cast<v2i*>(p.q + r * p.cols + c);
-      if constexpr (ONCE) __builtin_nontemporal_store(encode8(z[i], s, inv, p.fmt), q);
-      else *q = encode8(z[i], s, inv, p.fmt);
+      store_codes8<ONCE>(p.q + r * p.cols + c, encode8(z[i], s, inv, p.fmt));
       if (p.dz) store8<DK>(p.dz, r * p.cols + c, round8<DK>(z[i]));
     }
   }
@@ -234,11 +232,8 @@ int64_t partial_rows(int64_t rows, int64_t cols, int gran, int block_rows) {
   return few_rows(rows, cols) ? 1 : n;
 }
 
-// Inputs of 64 MB and more (twice the L2s) are loaded, and their codes stored,
-// nontemporally: 8192 x 8192 in BF16 at g = 128 73.4 -> 68.0 us, at g = 64 72.7
-// -> 69.4 us; a matrix of 16 MB was 5% slower that way.
-constexpr int64_t kOnceBytes = 64ll << 20;
-
+// kOnceBytes: 8192 x 8192 in BF16 at g = 128 73.4 -> 68.0 us nontemporally, at g
+// = 64 72.7 -> 69.4 us; a matrix of 16 MB was 5% slower that way.
 template <int DK, int ACT, int G, int NT>
 void launch_blocks(const EpiBwdArgs& p, float* part, hipStream_t stream) {
   const dim3 grid((unsigned)(((p.rows + G - 1) / G) * (p.cols / G)));

@@ -29,6 +29,11 @@
 #include "layer_ops.h"
 #include "quant_common.h"
 
+// Fused multiply-adds are written out, so that a row's result does not depend on
+// which of the kernels below its call takes (the row's sum has one order for
+// each row length up to the longest that registers hold).
+#pragma clang fp contract(off)
+
 namespace dg {
 
 namespace {
@@ -61,15 +66,15 @@ __device__ __forceinline__ float sum_sq8(const Raw8<K>& r) {
 }
 
 // h's eight elements from e_x of x and e_r of the residual, in h's kind.
-template <int XK, int RK>
+template <int XK, int RK, bool ONCE = false>
 __device__ __forceinline__ Raw8<RK == kAbsent ? XK : RK> stream8(const NormArgs& p, int64_t ex, int64_t er) {
-  const Raw8<XK> x = load8<XK>(p.x, ex);
+  const Raw8<XK> x = load8<XK, ONCE>(p.x, ex);
   if constexpr (RK == kAbsent) {
     return x;
   } else {
     float a[8], b[8];
     widen8(x, a);
-    widen8(load8<RK>(p.res, er), b);
+    widen8(load8<RK, ONCE>(p.res, er), b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] += b[i];
     return round8<RK>(a);
@@ -78,7 +83,7 @@ __device__ __forceinline__ Raw8<RK == kAbsent ? XK : RK> stream8(const NormArgs&
 
 // The outputs of eight elements of row `row` from column c on: segments are
 // whole lane groups (segment_max), so every lane of a group comes here.
-template <int XK, int HK>
+template <int XK, int HK, bool ONCE = false>
 __device__ __forceinline__ void emit8(const NormArgs& p, const Raw8<HK>& h, const float (&w)[8], float rstd, int64_t row,
                                       int c) {
   float y[8];
@@ -88,15 +93,15 @@ __device__ __forceinline__ void emit8(const NormArgs& p, const Raw8<HK>& h, cons
   const float amax = segment_max(amax8(y), p.gran);
   const float s = block_scale(amax, format_max(p.fmt));
   const int64_t e = row * p.cols + c;
-  *reinterpret_cast<v2i*>(p.q + e) = encode8(y, s, 1.0f / s, p.fmt);
+  store_codes8<ONCE>(p.q + e, encode8(y, s, 1.0f / s, p.fmt));
   if ((c & (p.gran - 1)) == 0) p.scales[row * p.segs + (c >> p.gshift)] = s;
-  if (p.y) store8<XK>(p.y, e, round8<XK>(y));
+  if (p.y) store8<XK, ONCE>(p.y, e, round8<XK>(y));
 }
 
 __device__ __forceinline__ void load_w8(const float* w, int c, float (&f)[8]) { widen8(load8<0>(w, c), f); }
 
 // RT threads per row, C eight-element chunks per thread (RT * C * 8 >= cols).
-template <int XK, int RK, int RT, int C>
+template <int XK, int RK, int RT, int C, bool ONCE>
 __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_quant(const NormArgs p) {
   constexpr int HK = RK == kAbsent ? XK : RK;
   constexpr int ROWS = RT < 256 ? 256 / RT : 1;
@@ -110,14 +115,14 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_quant(const NormA
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int ch = i * RT + t;
-    if (ch < chunks) h[i] = stream8<XK, RK>(p, row * p.ldx + 8 * ch, row * p.ldres + 8 * ch);
+    if (ch < chunks) h[i] = stream8<XK, RK, ONCE>(p, row * p.ldx + 8 * ch, row * p.ldres + 8 * ch);
   }
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int ch = i * RT + t;
     if (ch < chunks) {
       ss += sum_sq8(h[i]);
-      if (RK != kAbsent) store8<HK>(p.h, row * p.cols + 8 * ch, h[i]);
+      if (RK != kAbsent) store8<HK, ONCE>(p.h, row * p.cols + 8 * ch, h[i]);
     }
   }
   ss = row_sum<RT>(ss, red[team], t);
@@ -129,7 +134,7 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_quant(const NormA
     if (ch < chunks) {
       float w[8];
       load_w8(p.w, 8 * ch, w);
-      emit8<XK, HK>(p, h[i], w, rstd, row, 8 * ch);
+      emit8<XK, HK, ONCE>(p, h[i], w, rstd, row, 8 * ch);
     }
   }
 }
@@ -164,8 +169,13 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long(const NormArgs p) {
 template <int XK, int RK, int RT, int C>
 hipError_t launch_rows(const NormArgs& p, hipStream_t stream) {
   constexpr int ROWS = RT < 256 ? 256 / RT : 1;
-  hipLaunchKernelGGL((rmsnorm_quant<XK, RK, RT, C>), dim3((unsigned)((p.rows + ROWS - 1) / ROWS)),
-                     dim3(RT < 256 ? 256 : RT), 0, stream, p);
+  const dim3 grid((unsigned)((p.rows + ROWS - 1) / ROWS)), block(RT < 256 ? 256 : RT);
+  // kOnceBytes: 8192x8192 in BF16 85.6 -> 81.4 us nontemporally, 2622x14976
+  // (training) 69.9 -> 59.7, 4000x16384 85.0 -> 78.6; 300x4096 4.3 -> 4.5
+  if (p.rows * p.cols * (InKind<XK>::kBytes + (RK == kAbsent ? 0 : InKind<RK % kAbsent>::kBytes)) >= kOnceBytes)
+    hipLaunchKernelGGL((rmsnorm_quant<XK, RK, RT, C, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((rmsnorm_quant<XK, RK, RT, C, false>), grid, block, 0, stream, p);
   return hipGetLastError();
 }
 
@@ -200,11 +210,11 @@ hipError_t launch_norm_x(const NormArgs& p, hipStream_t stream) {
 
 // ---- backward -----------------------------------------------------------------
 
-// u * n and dy * n of eight elements: their contributions to the row's sum and
-// to the columns' sums.
+// s plus u * n of eight elements, one after the other.
 template <int DK, int HK>
-__device__ __forceinline__ float row_part8(const Raw8<DK>& dy, const Raw8<HK>& h, const float (&w)[8], float rstd) {
-  float g[8], n[8], s = 0.0f;
+__device__ __forceinline__ float row_part8(const Raw8<DK>& dy, const Raw8<HK>& h, const float (&w)[8], float rstd,
+                                            float s) {
+  float g[8], n[8];
   widen8(dy, g);
   widen8(h, n);
 #pragma unroll
@@ -213,7 +223,7 @@ __device__ __forceinline__ float row_part8(const Raw8<DK>& dy, const Raw8<HK>& h
 }
 
 // dx of eight elements from the row's mean of u * n.
-template <int DK, int HK>
+template <int DK, int HK, bool ONCE = false>
 __device__ __forceinline__ void store_dx8(const NormBwdArgs& p, const Raw8<DK>& dy, const Raw8<HK>& h, const Raw8<HK>& dh,
                                           const float (&w)[8], float rstd, float mean, int64_t e) {
   float g[8], n[8], d[8];
@@ -221,13 +231,13 @@ __device__ __forceinline__ void store_dx8(const NormBwdArgs& p, const Raw8<DK>& 
   widen8(h, n);
   widen8(dh, d);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) d[k] = __builtin_fmaf(rstd, g[k] * w[k] - n[k] * rstd * mean, d[k]);
-  store8<HK>(p.dx, e, round8<HK>(d));
+  for (int k = 0; k < 8; ++k) d[k] = __builtin_fmaf(rstd, __builtin_fmaf(-(n[k] * rstd), mean, g[k] * w[k]), d[k]);
+  store8<HK, ONCE>(p.dx, e, round8<HK>(d));
 }
 
-template <int HK>
+template <int HK, bool ONCE = false>
 __device__ __forceinline__ Raw8<HK> load_dh8(const NormBwdArgs& p, int64_t row, int c) {
-  return p.dh ? load8<HK>(p.dh, row * p.lddh + c) : Raw8<HK>{};
+  return p.dh ? load8<HK, ONCE>(p.dh, row * p.lddh + c) : Raw8<HK>{};
 }
 
 // Few rows, one launch and no workspace: the first `col_wgs` workgroups add
@@ -274,7 +284,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_few(const NormBwdArgs p, int
   }
 #pragma unroll
   for (int i = 0; i < C; ++i)
-    if (i * RT + t < chunks) s += row_part8<DK, HK>(dy[i], h[i], w[i], rstd);
+    if (i * RT + t < chunks) s = row_part8<DK, HK>(dy[i], h[i], w[i], rstd, s);
   s = row_sum<RT>(s, &red[0][0] + team * (RT / 64), t) / (float)p.cols;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -291,7 +301,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_few(const NormBwdArgs p, int
 // FP32 too, h as well, and w is read again for every row (from L2). A workgroup writes its
 // columns' sums as one partial row (its four teams' added through LDS where
 // RT = 64).
-template <int DK, int HK, int RT, int C>
+template <int DK, int HK, int RT, int C, bool ONCE>
 __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const NormBwdArgs p) {
   constexpr int NT = RT < 256 ? 256 : RT, TEAMS = NT / RT;
   __shared__ float red[2][RT / 64];
@@ -311,9 +321,9 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
     for (int i = 0; i < C; ++i) {
       const int ch = i * RT + t;
       if (ch < chunks) {
-        dy[i] = load8<DK>(p.dy, row * p.lddy + 8 * ch);
-        if (H_AHEAD) h[i] = load8<HK>(p.h, row * p.ldh + 8 * ch);
-        if (DH_AHEAD) dh[i] = load_dh8<HK>(p, row, 8 * ch);
+        dy[i] = load8<DK, ONCE>(p.dy, row * p.lddy + 8 * ch);
+        if (H_AHEAD) h[i] = load8<HK, ONCE>(p.h, row * p.ldh + 8 * ch);
+        if (DH_AHEAD) dh[i] = load_dh8<HK, ONCE>(p, row, 8 * ch);
       }
     }
   };
@@ -333,8 +343,8 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
       const int ch = i * RT + t;
       if (ch < chunks) {
         if (!KEEP_W) load_w8(p.w, 8 * ch, w[i]);
-        if (!H_AHEAD) h[i] = load8<HK>(p.h, row * p.ldh + 8 * ch);
-        if (!DH_AHEAD) dh[i] = load_dh8<HK>(p, row, 8 * ch);
+        if (!H_AHEAD) h[i] = load8<HK, ONCE>(p.h, row * p.ldh + 8 * ch);
+        if (!DH_AHEAD) dh[i] = load_dh8<HK, ONCE>(p, row, 8 * ch);
         float g[8], n[8];
         widen8(dy[i], g);
         widen8(h[i], n);
@@ -358,7 +368,7 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
       const int ch = i * RT + t;
       if (ch < chunks) {
         if (!KEEP_W) load_w8(p.w, 8 * ch, w[i]);
-        store_dx8<DK, HK>(p, dy[i], h[i], dh[i], w[i], rstd, s, row * p.cols + 8 * ch);
+        store_dx8<DK, HK, ONCE>(p, dy[i], h[i], dh[i], w[i], rstd, s, row * p.cols + 8 * ch);
       }
     }
     if (more) {
@@ -407,7 +417,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_rows_long(const NormBwdArgs 
   for (int ch = threadIdx.x; ch < chunks; ch += RT) {
     float w[8];
     load_w8(p.w, 8 * ch, w);
-    s += row_part8<DK, HK>(load8<DK>(p.dy, row * p.lddy + 8 * ch), load8<HK>(p.h, row * p.ldh + 8 * ch), w, rstd);
+    s = row_part8<DK, HK>(load8<DK>(p.dy, row * p.lddy + 8 * ch), load8<HK>(p.h, row * p.ldh + 8 * ch), w, rstd, s);
   }
   s = row_sum<RT>(s, red, (int)threadIdx.x) / (float)p.cols;
   for (int ch = threadIdx.x; ch < chunks; ch += RT) {
@@ -495,7 +505,17 @@ void launch_bwd(const NormBwdArgs& p, const BwdPlan& b, hipStream_t stream) {
     hipLaunchKernelGGL((rmsnorm_bwd_few<DK, HK, RT, C>), dim3((unsigned)(col_wgs + (p.rows + ROWS - 1) / ROWS)), dim3(1024), 0,
                        stream, p, col_wgs);
   } else {
-    hipLaunchKernelGGL((rmsnorm_bwd_many<DK, HK, RT, C>), dim3((unsigned)b.partial), dim3(RT < 256 ? 256 : RT), 0, stream, p);
+    // From 128 MB of inputs on nontemporally: 8192x8192 in BF16 100.8 -> 90.6 us,
+    // 7459x5376 64.8 -> 61.7, 2000x16384 with an FP32 stream 96.4 -> 92.7 (967x9600
+    // with one, 93 MB: 32.1 -> 33.9); not where w is read for every row (FP32 dy
+    // and stream, 2000x16384: 111 -> 118).
+    constexpr bool W_AGAIN = C > 1 && DK == 0 && HK == 0;
+    const dim3 grid((unsigned)b.partial), block(RT < 256 ? 256 : RT);
+    const int64_t bytes = p.rows * p.cols * (InKind<DK>::kBytes + (p.dh ? 2 : 1) * InKind<HK>::kBytes);
+    if (!W_AGAIN && bytes >= 2 * kOnceBytes)
+      hipLaunchKernelGGL((rmsnorm_bwd_many<DK, HK, RT, C, !W_AGAIN>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((rmsnorm_bwd_many<DK, HK, RT, C, false>), grid, block, 0, stream, p);
   }
 }
 

@@ -152,6 +152,10 @@ __device__ __forceinline__ int encode4(v4f v, float s, float inv) {
   }
 }
 
+// Inputs of 64 MB and more, twice the L2s, are read and the outputs made from
+// them written nontemporally (ONCE below).
+constexpr int64_t kOnceBytes = 64ll << 20;
+
 // Eight consecutive elements of kind K as loaded (one or two 16-byte words),
 // so that a value waiting for its row's reduction costs 4 registers for 16-bit
 // kinds, not 8.
@@ -161,7 +165,8 @@ struct Raw8 {
 };
 
 // p: base of a matrix of kind K; e: index of the first element (the address
-// is 16-byte aligned). ONCE: data read once and larger than the caches.
+// is 16-byte aligned). ONCE (here and below): nontemporal, for data that is
+// larger than the caches.
 template <int K, bool ONCE = false>
 __device__ __forceinline__ Raw8<K> load8(const void* p, int64_t e) {
   Raw8<K> r;
@@ -204,11 +209,20 @@ __device__ __forceinline__ Raw8<K> round8(const float (&f)[8]) {
   return r;
 }
 
-template <int K>
+template <int K, bool ONCE = false>
 __device__ __forceinline__ void store8(void* p, int64_t e, const Raw8<K>& r) {
   v4u* dst = reinterpret_cast<v4u*>(static_cast<char*>(p) + e * InKind<K>::kBytes);
 #pragma unroll
-  for (int i = 0; i < InKind<K>::kBytes / 2; ++i) dst[i] = r.w[i];
+  for (int i = 0; i < InKind<K>::kBytes / 2; ++i) {
+    if constexpr (ONCE) __builtin_nontemporal_store(r.w[i], dst + i);
+    else dst[i] = r.w[i];
+  }
+}
+
+template <bool ONCE>
+__device__ __forceinline__ void store_codes8(uint8_t* q, v2i codes) {
+  if constexpr (ONCE) __builtin_nontemporal_store(codes, reinterpret_cast<v2i*>(q));
+  else *reinterpret_cast<v2i*>(q) = codes;
 }
 
 // Max over the lanes that share a g-wide segment when a lane holds eight of

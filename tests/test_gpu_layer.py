@@ -509,6 +509,40 @@ def test_short_way_refuses_the_same(dg):
                                dweight=torch.empty_like(w), workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
 
 
+@pytest.mark.parametrize("rows,cols", [(70000, 512), (36000, 1024), (18000, 2048), (9000, 4096), (4500, 8192), (2300, 16384)])
+def test_large_calls_equal_their_parts(dg, rows, cols):
+    """A matrix past the size from which data bypasses the caches gives what its row slices, below that size, give."""
+    gen = torch.Generator(device=DEV).manual_seed(rows)
+    x, res, dy = (torch.randn(rows, cols, generator=gen, device=DEV).to(BF16) for _ in range(3))
+    w = weight(cols).to(DEV)
+    y, rstd = torch.empty_like(x), torch.empty(rows, device=DEV)
+    say("large calls %dx%d" % (rows, cols))
+    q, s, h = dg.dg_rmsnorm_quantize_fp8(x, res, w, gran=64, y=y, rstd=rstd)
+    dx, dw = dg.dg_rmsnorm_backward(dy, h, rstd, w, dh=res)
+    eq, es = dg.dg_epilogue_backward_fp8(dy, x, dg.DG_ACT_SILU, gran=64, block_rows=1)
+    bq, bs = dg.dg_epilogue_backward_fp8(dy, x, dg.DG_ACT_SILU, gran=64)
+    torch.cuda.synchronize()
+    total, size = torch.zeros(cols, dtype=torch.float64, device=DEV), torch.zeros(cols, dtype=torch.float64, device=DEV)
+    step = -(-rows // 9 // 64) * 64
+    for r in range(0, rows, step):
+        at = slice(r, min(r + step, rows))
+        py, pr = torch.empty_like(x[at]), torch.empty_like(rstd[at])
+        pq, ps, ph = dg.dg_rmsnorm_quantize_fp8(x[at], res[at], w, gran=64, y=py, rstd=pr)
+        for got, want in ((pq, q), (ps, s), (ph, h), (py, y), (pr, rstd)):
+            assert torch.equal(got, want[at])
+        px, _ = dg.dg_rmsnorm_backward(dy[at], h[at], rstd[at], w, dh=res[at])
+        assert torch.equal(px, dx[at])
+        pq, ps = dg.dg_epilogue_backward_fp8(dy[at], x[at], dg.DG_ACT_SILU, gran=64, block_rows=1)
+        assert torch.equal(pq, eq[at]) and torch.equal(ps, es[at])
+        pq, ps = dg.dg_epilogue_backward_fp8(dy[at], x[at], dg.DG_ACT_SILU, gran=64)
+        assert torch.equal(pq, bq[at]) and torch.equal(ps, bs[r // 64 : r // 64 + ps.shape[0]])
+        terms = dy[at].double() * (h[at].double() * rstd[at].double()[:, None])
+        total += terms.sum(0)
+        size += terms.abs().sum(0)
+    # a column's terms are added in chains of at most rows / 64, then by trees of depth below 96
+    assert ((dw.double() - total).abs() <= (rows / 64 + 96) * ref.U32 * size).all()
+
+
 def test_offsets_past_32_bits(dg):
     """More than 2^32 elements: the last rows against the reference on those rows."""
     rows, cols, n = (1 << 19) + 5, 8192, 4
