@@ -26,24 +26,24 @@ namespace dg {
 
 namespace {
 
-// dz of eight elements (ACT 0: dout itself).
-template <int DK, int ACT>
-__device__ __forceinline__ void grad8(const Raw8<DK>& dout, const Raw8<1>& pre, float (&z)[8]) {
-  widen8(dout, z);
+// dz of E elements (ACT 0: dout itself).
+template <int ACT, int DK, int E>
+__device__ __forceinline__ void grad(const Raw<DK, E>& dout, const Raw<1, E>& pre, float (&z)[E]) {
+  widen_raw(dout, z);
   if constexpr (ACT != 0) {
-    float f[8];
-    widen8(pre, f);
+    float f[E];
+    widen_raw(pre, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] *= act_grad<ACT>(f[i]);
+    for (int i = 0; i < E; ++i) z[i] *= act_grad<ACT>(f[i]);
   }
 }
 
-template <int DK, int ACT, bool ONCE = false>
-__device__ __forceinline__ void grad8(const EpiBwdArgs& p, int64_t row, int64_t c, float (&z)[8]) {
-  const Raw8<DK> dout = load8<DK, ONCE>(p.dout, row * p.lddout + c);
-  Raw8<1> pre = {};
-  if constexpr (ACT != 0) pre = load8<1, ONCE>(p.pre, row * p.ldpre + c);
-  grad8<DK, ACT>(dout, pre, z);
+template <int DK, int ACT, int E, bool ONCE = false>
+__device__ __forceinline__ void grad(const EpiBwdArgs& p, int64_t row, int64_t c, float (&z)[E]) {
+  const Raw<DK, E> dout = load_raw<DK, E, ONCE>(p.dout, row * p.lddout + c);
+  Raw<1, E> pre = {};
+  if constexpr (ACT != 0) pre = load_raw<1, E, ONCE>(p.pre, row * p.ldpre + c);
+  grad<ACT>(dout, pre, z);
 }
 
 // Where the launches are short, dbias without a second one: the first workgroups
@@ -64,18 +64,18 @@ __device__ __forceinline__ void few_rows_dbias(const EpiBwdArgs& p, int group) {
   for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
   constexpr int U = 2;  // rows in flight per thread
   for (int64_t r0 = rl; r0 < p.rows; r0 += U * RL) {
-    Raw8<DK> d[U];
-    Raw8<1> pre[U];
+    Raw<DK, 8> d[U];
+    Raw<1, 8> pre[U] = {};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = r0 + u * RL < p.rows ? r0 + u * RL : r0;  // past the end: a row again, not counted
-      d[u] = load8<DK>(p.dout, r * p.lddout + c);
-      if (ACT != 0) pre[u] = load8<1>(p.pre, r * p.ldpre + c);
+      d[u] = load_raw<DK, 8>(p.dout, r * p.lddout + c);
+      if (ACT != 0) pre[u] = load_raw<1, 8>(p.pre, r * p.ldpre + c);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float z[8];
-      grad8<DK, ACT>(d[u], pre[u], z);
+      grad<ACT>(d[u], pre[u], z);
       if (r0 + u * RL < p.rows) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] += z[k];
@@ -106,7 +106,8 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
     if ((int)blockIdx.x < col_wgs) return few_rows_dbias<DK, ACT, NT>(p, blockIdx.x);
   }
   const int block = blockIdx.x - (FORM == kFew ? col_wgs : 0);
-  constexpr int ROW_L = G / 8;    // lanes per block row
+  constexpr int E = 8;  // four for FP32: twice the passes, 8192 x 8192 81.6 -> 85.2 us
+  constexpr int ROW_L = G / E;    // lanes per block row
   constexpr int RPP = NT / ROW_L;  // block rows covered by one pass
   constexpr int PASSES = G / RPP;
   static_assert(PASSES * RPP == G, "passes");
@@ -115,27 +116,27 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
   const int ncb = (int)(p.cols / G);
   const int rb = block / ncb, cb = block % ncb;
   const int t = threadIdx.x, rsub = t / ROW_L, cl = t % ROW_L;
-  const int64_t c = (int64_t)cb * G + cl * 8;
+  const int64_t c = (int64_t)cb * G + cl * E;
 
-  float z[PASSES][8], acc[8];
+  float z[PASSES][E], acc[E];
   float amax = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+  for (int k = 0; k < E; ++k) acc[k] = 0.0f;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int64_t r = (int64_t)rb * G + i * RPP + rsub;
     if (r < p.rows) {
-      grad8<DK, ACT, ONCE>(p, r, c, z[i]);
-      amax = fmaxf(amax, amax8(z[i]));
+      grad<DK, ACT, E, ONCE>(p, r, c, z[i]);
+      amax = fmaxf(amax, amax_of(z[i]));
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += z[i][k];
+      for (int k = 0; k < E; ++k) acc[k] += z[i][k];
     }
   }
   amax = group_max<64>(amax);
   if ((t & 63) == 0) red[t >> 6] = amax;
   if (FORM != kFew && part) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sums[rsub][cl * 8 + k] = acc[k];
+    for (int k = 0; k < E; ++k) sums[rsub][cl * E + k] = acc[k];
   }
   __syncthreads();
   amax = red[0];
@@ -148,8 +149,8 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
   for (int i = 0; i < PASSES; ++i) {
     const int64_t r = (int64_t)rb * G + i * RPP + rsub;
     if (r < p.rows) {
-      store_codes8<ONCE>(p.q + r * p.cols + c, encode8(z[i], s, inv, p.fmt));
-      if (p.dz) store8<DK>(p.dz, r * p.cols + c, round8<DK>(z[i]));
+      store_codes<ONCE>(p.q + r * p.cols + c, z[i], s, inv, p.fmt);
+      if (p.dz) store_raw<ONCE>(p.dz, r * p.cols + c, round_raw<DK>(z[i]));
     }
   }
   if (FORM != kFew && part && t < G) {
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
   }
 }
 
-// 1 x g: 512 columns per workgroup, its 16 waves (NW) a row each. The rows a
+// 1 x g: 64 units of columns per workgroup, its 16 waves (NW) a row each. The rows a
 // workgroup takes lie ranges * NW apart, so that all workgroups advance through
 // memory together: contiguous row ranges kept 128 distant places of it open at
 // once and took 86 us where this takes 78 (8192 x 8192, BF16, GELU). Several
@@ -168,6 +169,7 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
 // same but for more partial rows (2000 x 7168, FP32: 23.0 us at 4 waves, 21.3
 // at 16).
 constexpr int NW = 16;
+constexpr int row_cols(int dk) { return 64 * unit_of(dk, 1); }  // columns of a workgroup
 
 template <int DK, int ACT, int FORM>
 __global__ __launch_bounds__(64 * NW) void epi_bwd_rows(const EpiBwdArgs p, float* part, int col_groups, int ranges,
@@ -176,33 +178,34 @@ __global__ __launch_bounds__(64 * NW) void epi_bwd_rows(const EpiBwdArgs p, floa
     if ((int)blockIdx.x < col_wgs) return few_rows_dbias<DK, ACT, 64 * NW>(p, blockIdx.x);
   }
   const int block = blockIdx.x - (FORM == kFew ? col_wgs : 0);
-  __shared__ float sums[FORM == kFew ? 1 : NW][512];
+  constexpr int E = unit_of(DK, 1), COLS = row_cols(DK);
+  __shared__ float sums[FORM == kFew ? 1 : NW][COLS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int cg = block % col_groups, rr = block / col_groups;
-  const int64_t c = (int64_t)cg * 512 + lane * 8;
+  const int64_t c = (int64_t)cg * COLS + lane * E;
   const int gshift = 31 - __builtin_clz(p.gran);
   const int64_t segs = p.cols >> gshift;
-  float acc[8];
+  float acc[E];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+  for (int k = 0; k < E; ++k) acc[k] = 0.0f;
   if (c < p.cols) {  // whole segments are live or not, so each reduction stays inside live lanes
     for (int64_t r = (int64_t)NW * rr + wave; r < p.rows; r += (int64_t)NW * ranges) {
-      float z[8];
-      grad8<DK, ACT>(p, r, c, z);
+      float z[E];
+      grad<DK, ACT>(p, r, c, z);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += z[k];
-      const float s = block_scale(segment_max(amax8(z), p.gran), format_max(p.fmt));
-      *reinterpret_cast<v2i*>(p.q + r * p.cols + c) = encode8(z, s, 1.0f / s, p.fmt);
+      for (int k = 0; k < E; ++k) acc[k] += z[k];
+      const float s = block_scale(segment_max<E>(amax_of(z), p.gran), format_max(p.fmt));
+      store_codes(p.q + r * p.cols + c, z, s, 1.0f / s, p.fmt);
       if (((int)c & (p.gran - 1)) == 0) p.scales[r * segs + (c >> gshift)] = s;
-      if (p.dz) store8<DK>(p.dz, r * p.cols + c, round8<DK>(z));
+      if (p.dz) store_raw(p.dz, r * p.cols + c, round_raw<DK>(z));
     }
   }
   if (FORM == kFew || !part) return;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sums[wave][lane * 8 + k] = acc[k];
+  for (int k = 0; k < E; ++k) sums[wave][lane * E + k] = acc[k];
   __syncthreads();
-  const int64_t col = (int64_t)cg * 512 + threadIdx.x;
-  if (threadIdx.x < 512 && col < p.cols) {
+  const int64_t col = (int64_t)cg * COLS + threadIdx.x;
+  if (threadIdx.x < COLS && col < p.cols) {
     float v = sums[0][threadIdx.x];
 #pragma unroll
     for (int w = 1; w < NW; ++w) v += sums[w][threadIdx.x];
@@ -212,8 +215,8 @@ __global__ __launch_bounds__(64 * NW) void epi_bwd_rows(const EpiBwdArgs p, floa
 
 // Row ranges of the 1 x g form: two workgroups per CU over all, a row per wave at
 // least.
-int64_t row_ranges(int64_t rows, int64_t cols) {
-  const int64_t r = 512 / ((cols + 511) / 512), most = (rows + NW - 1) / NW;
+int64_t row_ranges(int64_t rows, int64_t cols, int dk) {
+  const int64_t r = 512 / ((cols + row_cols(dk) - 1) / row_cols(dk)), most = (rows + NW - 1) / NW;
   return r < 1 ? 1 : r < most ? r : most;
 }
 
@@ -227,8 +230,8 @@ bool few_rows(int64_t rows, int64_t cols) { return rows <= kFewRows && rows * co
 
 // Partial rows of dbias (one: the sums go straight to it): a row of blocks each
 // (g x g), or a row range each (1 x g).
-int64_t partial_rows(int64_t rows, int64_t cols, int gran, int block_rows) {
-  const int64_t n = block_rows == 1 ? row_ranges(rows, cols) : (rows + gran - 1) / gran;
+int64_t partial_rows(int64_t rows, int64_t cols, int gran, int block_rows, int dk) {
+  const int64_t n = block_rows == 1 ? row_ranges(rows, cols, dk) : (rows + gran - 1) / gran;
   return few_rows(rows, cols) ? 1 : n;
 }
 
@@ -258,10 +261,10 @@ void launch_blocks_few(const EpiBwdArgs& p, int col_wgs, hipStream_t stream) {
 // workgroups overlap their loads and stores less.
 template <int DK, int ACT>
 hipError_t launch_act(const EpiBwdArgs& p, hipStream_t stream) {
-  const int64_t n = partial_rows(p.rows, p.cols, p.gran, p.block_rows);
+  const int64_t n = partial_rows(p.rows, p.cols, p.gran, p.block_rows, DK);
   float* part = !p.dbias ? nullptr : n > 1 ? p.ws : p.dbias;
   // one row of blocks (or one range) has dbias' sums already
-  const int64_t ranges = row_ranges(p.rows, p.cols);
+  const int64_t ranges = row_ranges(p.rows, p.cols, DK);
   bool few = p.dbias && few_rows(p.rows, p.cols) && (p.block_rows == 1 ? ranges > 1 : p.rows > p.gran);
   if (few && p.dz == p.dout) {
     const dim3 grid((unsigned)(p.cols / kFewCols));
@@ -273,7 +276,7 @@ hipError_t launch_act(const EpiBwdArgs& p, hipStream_t stream) {
   const int col_wgs = few ? (int)(p.cols / kFewCols) : 0;
   const int64_t blocks = ((p.rows + p.gran - 1) / p.gran) * (p.cols / p.gran);
   if (p.block_rows == 1) {
-    const int64_t col_groups = (p.cols + 511) / 512;
+    const int64_t col_groups = (p.cols + row_cols(DK) - 1) / row_cols(DK);
     const dim3 grid((unsigned)(col_groups * ranges + col_wgs));
     if (few)
       hipLaunchKernelGGL((epi_bwd_rows<DK, ACT, kFew>), grid, dim3(64 * NW), 0, stream, p, nullptr, (int)col_groups,
@@ -312,7 +315,7 @@ hipError_t launch_kind(const EpiBwdArgs& p, hipStream_t stream) {
 }  // namespace
 
 int64_t epi_bwd_workspace(int64_t rows, int64_t cols, int gran, int block_rows) {
-  const int64_t n = partial_rows(rows, cols, gran, block_rows);
+  const int64_t n = partial_rows(rows, cols, gran, block_rows, 1);  // 16-bit types have at least FP32's ranges
   return n > 1 ? n * cols * (int64_t)sizeof(float) : 0;
 }
 

@@ -55,88 +55,86 @@ __device__ __forceinline__ float row_sum(float v, float* red, int t) {
   return v;
 }
 
-template <int K>
-__device__ __forceinline__ float sum_sq8(const Raw8<K>& r) {
-  float f[8];
-  widen8(r, f);
-  float s = 0.0f;
+template <int K, int E>
+__device__ __forceinline__ float sum_sq(const Raw<K, E>& r, float s) {
+  float f[E];
+  widen_raw(r, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s = __builtin_fmaf(f[i], f[i], s);
+  for (int i = 0; i < E; ++i) s = __builtin_fmaf(f[i], f[i], s);
   return s;
 }
 
-// h's eight elements from e_x of x and e_r of the residual, in h's kind.
-template <int XK, int RK, bool ONCE = false>
-__device__ __forceinline__ Raw8<RK == kAbsent ? XK : RK> stream8(const NormArgs& p, int64_t ex, int64_t er) {
-  const Raw8<XK> x = load8<XK, ONCE>(p.x, ex);
+// h's elements from ex of x and er of the residual on, in h's kind.
+template <int XK, int RK, int E, bool ONCE = false>
+__device__ __forceinline__ Raw<RK == kAbsent ? XK : RK, E> stream_of(const NormArgs& p, int64_t ex, int64_t er) {
+  const Raw<XK, E> x = load_raw<XK, E, ONCE>(p.x, ex);
   if constexpr (RK == kAbsent) {
     return x;
   } else {
-    float a[8], b[8];
-    widen8(x, a);
-    widen8(load8<RK, ONCE>(p.res, er), b);
+    float a[E], b[E];
+    widen_raw(x, a);
+    widen_raw(load_raw<RK, E, ONCE>(p.res, er), b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] += b[i];
-    return round8<RK>(a);
+    for (int i = 0; i < E; ++i) a[i] += b[i];
+    return round_raw<RK>(a);
   }
 }
 
-// The outputs of eight elements of row `row` from column c on: segments are
-// whole lane groups (segment_max), so every lane of a group comes here.
-template <int XK, int HK, bool ONCE = false>
-__device__ __forceinline__ void emit8(const NormArgs& p, const Raw8<HK>& h, const float (&w)[8], float rstd, int64_t row,
-                                      int c) {
-  float y[8];
-  widen8(h, y);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = y[i] * rstd * w[i];
-  const float amax = segment_max(amax8(y), p.gran);
-  const float s = block_scale(amax, format_max(p.fmt));
-  const int64_t e = row * p.cols + c;
-  store_codes8<ONCE>(p.q + e, encode8(y, s, 1.0f / s, p.fmt));
-  if ((c & (p.gran - 1)) == 0) p.scales[row * p.segs + (c >> p.gshift)] = s;
-  if (p.y) store8<XK, ONCE>(p.y, e, round8<XK>(y));
+template <int E>
+__device__ __forceinline__ void load_w(const float* w, int c, float (&f)[E]) {
+  widen_raw(load_raw<0, E>(w, c), f);
 }
 
-__device__ __forceinline__ void load_w8(const float* w, int c, float (&f)[8]) { widen8(load8<0>(w, c), f); }
+// The outputs of E elements of row `row` from column c on: segments are whole
+// lane groups (segment_max), so every lane of a group comes here.
+template <int XK, int HK, int E, bool ONCE = false>
+__device__ __forceinline__ void emit(const NormArgs& p, const Raw<HK, E>& h, float rstd, int64_t row, int c) {
+  float y[E], w[E];
+  load_w(p.w, c, w);
+  widen_raw(h, y);
+#pragma unroll
+  for (int i = 0; i < E; ++i) y[i] = y[i] * rstd * w[i];
+  const float amax = segment_max<E>(amax_of(y), p.gran);
+  const float s = block_scale(amax, format_max(p.fmt));
+  const int64_t e = row * p.cols + c;
+  store_codes<ONCE>(p.q + e, y, s, 1.0f / s, p.fmt);
+  if ((c & (p.gran - 1)) == 0) p.scales[row * p.segs + (c >> p.gshift)] = s;
+  if (p.y) store_raw<ONCE>(p.y, e, round_raw<XK>(y));
+}
 
-// RT threads per row, C eight-element chunks per thread (RT * C * 8 >= cols).
+constexpr int unit_of_norm(int xk, int rk) { return unit_of(xk, rk == kAbsent ? xk : rk); }
+
+// RT threads per row, 8 C elements per thread (RT * C * 8 >= cols) in units of E
+// elements.
 template <int XK, int RK, int RT, int C, bool ONCE>
 __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_quant(const NormArgs p) {
-  constexpr int HK = RK == kAbsent ? XK : RK;
+  constexpr int HK = RK == kAbsent ? XK : RK, E = unit_of_norm(XK, RK), U = 8 * C / E;
   constexpr int ROWS = RT < 256 ? 256 / RT : 1;
   __shared__ float red[ROWS][RT / 64];
   const int t = threadIdx.x % RT, team = threadIdx.x / RT;
   const int64_t row = (int64_t)blockIdx.x * ROWS + team;
   if (RT == 64 && row >= p.rows) return;  // whole waves, and no barrier follows
-  const int chunks = row < p.rows ? (int)(p.cols / 8) : 0;  // a team past the last row only meets the barrier
-  Raw8<HK> h[C];
+  const int units = row < p.rows ? (int)(p.cols / E) : 0;  // a team past the last row only meets the barrier
+  Raw<HK, E> h[U];
   float ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int ch = i * RT + t;
-    if (ch < chunks) h[i] = stream8<XK, RK, ONCE>(p, row * p.ldx + 8 * ch, row * p.ldres + 8 * ch);
+  for (int i = 0; i < U; ++i) {
+    const int c = E * (i * RT + t);
+    if (i * RT + t < units) h[i] = stream_of<XK, RK, E, ONCE>(p, row * p.ldx + c, row * p.ldres + c);
   }
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int ch = i * RT + t;
-    if (ch < chunks) {
-      ss += sum_sq8(h[i]);
-      if (RK != kAbsent) store8<HK, ONCE>(p.h, row * p.cols + 8 * ch, h[i]);
+  for (int i = 0; i < U; ++i) {
+    if (i * RT + t < units) {
+      ss = sum_sq(h[i], ss);
+      if (RK != kAbsent) store_raw<ONCE>(p.h, row * p.cols + E * (i * RT + t), h[i]);
     }
   }
   ss = row_sum<RT>(ss, red[team], t);
   const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
-  if (p.rstd && t == 0 && chunks) p.rstd[row] = rstd;
+  if (p.rstd && t == 0 && units) p.rstd[row] = rstd;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int ch = i * RT + t;
-    if (ch < chunks) {
-      float w[8];
-      load_w8(p.w, 8 * ch, w);
-      emit8<XK, HK, ONCE>(p, h[i], w, rstd, row, 8 * ch);
-    }
-  }
+  for (int i = 0; i < U; ++i)
+    if (i * RT + t < units) emit<XK, HK, E, ONCE>(p, h[i], rstd, row, E * (i * RT + t));
 }
 
 // Rows longer than the registers of a workgroup hold: the row is read twice,
@@ -144,25 +142,23 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_quant(const NormA
 // each thread reads what it wrote itself).
 template <int XK, int RK>
 __global__ __launch_bounds__(1024) void rmsnorm_quant_long(const NormArgs p) {
-  constexpr int HK = RK == kAbsent ? XK : RK, RT = 1024;
+  constexpr int HK = RK == kAbsent ? XK : RK, RT = 1024, E = unit_of_norm(XK, RK);
   __shared__ float red[RT / 64];
-  const int t = threadIdx.x;
   const int64_t row = blockIdx.x;
-  const int chunks = (int)(p.cols / 8);
+  const int units = (int)(p.cols / E);
   float ss = 0.0f;
-  for (int ch = t; ch < chunks; ch += RT) {
-    const Raw8<HK> h = stream8<XK, RK>(p, row * p.ldx + 8 * ch, row * p.ldres + 8 * ch);
-    ss += sum_sq8(h);
-    if (RK != kAbsent) store8<HK>(p.h, row * p.cols + 8 * ch, h);
+  for (int u = threadIdx.x; u < units; u += RT) {
+    const Raw<HK, E> h = stream_of<XK, RK, E>(p, row * p.ldx + E * u, row * p.ldres + E * u);
+    ss = sum_sq(h, ss);
+    if (RK != kAbsent) store_raw(p.h, row * p.cols + E * u, h);
   }
-  ss = row_sum<RT>(ss, red, t);
+  ss = row_sum<RT>(ss, red, (int)threadIdx.x);
   const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
-  if (p.rstd && t == 0) p.rstd[row] = rstd;
-  for (int ch = t; ch < chunks; ch += RT) {
-    float w[8];
-    load_w8(p.w, 8 * ch, w);
-    const Raw8<HK> h = RK == kAbsent ? load8<HK>(p.x, row * p.ldx + 8 * ch) : load8<HK>(p.h, row * p.cols + 8 * ch);
-    emit8<XK, HK>(p, h, w, rstd, row, 8 * ch);
+  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  for (int u = threadIdx.x; u < units; u += RT) {
+    const Raw<HK, E> h =
+        RK == kAbsent ? load_raw<HK, E>(p.x, row * p.ldx + E * u) : load_raw<HK, E>(p.h, row * p.cols + E * u);
+    emit<XK, HK, E>(p, h, rstd, row, E * u);
   }
 }
 
@@ -210,34 +206,33 @@ hipError_t launch_norm_x(const NormArgs& p, hipStream_t stream) {
 
 // ---- backward -----------------------------------------------------------------
 
-// s plus u * n of eight elements, one after the other.
-template <int DK, int HK>
-__device__ __forceinline__ float row_part8(const Raw8<DK>& dy, const Raw8<HK>& h, const float (&w)[8], float rstd,
-                                            float s) {
-  float g[8], n[8];
-  widen8(dy, g);
-  widen8(h, n);
+// s plus u * n of E elements, one after the other.
+template <int DK, int HK, int E>
+__device__ __forceinline__ float row_part(const Raw<DK, E>& dy, const Raw<HK, E>& h, const float (&w)[E], float rstd, float s) {
+  float g[E], n[E];
+  widen_raw(dy, g);
+  widen_raw(h, n);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s = __builtin_fmaf(g[k] * w[k], n[k] * rstd, s);
+  for (int k = 0; k < E; ++k) s = __builtin_fmaf(g[k] * w[k], n[k] * rstd, s);
   return s;
 }
 
-// dx of eight elements from the row's mean of u * n.
-template <int DK, int HK, bool ONCE = false>
-__device__ __forceinline__ void store_dx8(const NormBwdArgs& p, const Raw8<DK>& dy, const Raw8<HK>& h, const Raw8<HK>& dh,
-                                          const float (&w)[8], float rstd, float mean, int64_t e) {
-  float g[8], n[8], d[8];
-  widen8(dy, g);
-  widen8(h, n);
-  widen8(dh, d);
+// dx of E elements from the row's mean of u * n.
+template <bool ONCE = false, int DK, int HK, int E>
+__device__ __forceinline__ void store_dx(const NormBwdArgs& p, const Raw<DK, E>& dy, const Raw<HK, E>& h, const Raw<HK, E>& dh,
+                                         const float (&w)[E], float rstd, float mean, int64_t e) {
+  float g[E], n[E], d[E];
+  widen_raw(dy, g);
+  widen_raw(h, n);
+  widen_raw(dh, d);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) d[k] = __builtin_fmaf(rstd, __builtin_fmaf(-(n[k] * rstd), mean, g[k] * w[k]), d[k]);
-  store8<HK, ONCE>(p.dx, e, round8<HK>(d));
+  for (int k = 0; k < E; ++k) d[k] = __builtin_fmaf(rstd, __builtin_fmaf(-(n[k] * rstd), mean, g[k] * w[k]), d[k]);
+  store_raw<ONCE>(p.dx, e, round_raw<HK>(d));
 }
 
-template <int HK, bool ONCE = false>
-__device__ __forceinline__ Raw8<HK> load_dh8(const NormBwdArgs& p, int64_t row, int c) {
-  return p.dh ? load8<HK, ONCE>(p.dh, row * p.lddh + c) : Raw8<HK>{};
+template <int HK, int E, bool ONCE = false>
+__device__ __forceinline__ Raw<HK, E> load_dh(const NormBwdArgs& p, int64_t row, int c) {
+  return p.dh ? load_raw<HK, E, ONCE>(p.dh, row * p.lddh + c) : Raw<HK, E>{};
 }
 
 // Few rows, one launch and no workspace: the first `col_wgs` workgroups add
@@ -256,8 +251,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_few(const NormBwdArgs p, int
 #pragma unroll 4
     for (int64_t r = rl; r < p.rows; r += RL) {
       float g[8], h[8];
-      widen8(load8<DK>(p.dy, r * p.lddy + c), g);
-      widen8(load8<HK>(p.h, r * p.ldh + c), h);
+      widen_raw(load_raw<DK, 8>(p.dy, r * p.lddy + c), g);
+      widen_raw(load_raw<HK, 8>(p.h, r * p.ldh + c), h);
       const float rstd = p.rstd[r];
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(g[k], h[k] * rstd, acc[k]);
@@ -267,30 +262,29 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_few(const NormBwdArgs p, int
   }
   const int t = threadIdx.x % RT, team = threadIdx.x / RT;
   const int64_t row = (int64_t)(blockIdx.x - col_wgs) * ROWS + team;
-  const int chunks = row < p.rows ? (int)(p.cols / 8) : 0;  // a team past the last row only meets the barrier
-  const float rstd = chunks ? p.rstd[row] : 0.0f;
-  Raw8<DK> dy[C];
-  Raw8<HK> h[C], dh[C];
-  float w[C][8], s = 0.0f;
+  constexpr int E = unit_of(DK, HK), U = 8 * C / E;
+  const int units = row < p.rows ? (int)(p.cols / E) : 0;  // a team past the last row only meets the barrier
+  const float rstd = units ? p.rstd[row] : 0.0f;
+  Raw<DK, E> dy[U];
+  Raw<HK, E> h[U], dh[U];
+  float w[U][E], s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int ch = i * RT + t;
-    if (ch < chunks) {
-      dy[i] = load8<DK>(p.dy, row * p.lddy + 8 * ch);
-      h[i] = load8<HK>(p.h, row * p.ldh + 8 * ch);
-      dh[i] = load_dh8<HK>(p, row, 8 * ch);
-      load_w8(p.w, 8 * ch, w[i]);
+  for (int i = 0; i < U; ++i) {
+    const int c = E * (i * RT + t);
+    if (i * RT + t < units) {
+      dy[i] = load_raw<DK, E>(p.dy, row * p.lddy + c);
+      h[i] = load_raw<HK, E>(p.h, row * p.ldh + c);
+      dh[i] = load_dh<HK, E>(p, row, c);
+      load_w(p.w, c, w[i]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < C; ++i)
-    if (i * RT + t < chunks) s = row_part8<DK, HK>(dy[i], h[i], w[i], rstd, s);
+  for (int i = 0; i < U; ++i)
+    if (i * RT + t < units) s = row_part(dy[i], h[i], w[i], rstd, s);
   s = row_sum<RT>(s, &red[0][0] + team * (RT / 64), t) / (float)p.cols;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int ch = i * RT + t;
-    if (ch < chunks) store_dx8<DK, HK>(p, dy[i], h[i], dh[i], w[i], rstd, s, row * p.cols + 8 * ch);
-  }
+  for (int i = 0; i < U; ++i)
+    if (i * RT + t < units) store_dx(p, dy[i], h[i], dh[i], w[i], rstd, s, row * p.cols + E * (i * RT + t));
 }
 
 // Many rows: every team of RT threads takes rows team, team + teams, ...; its
@@ -306,74 +300,74 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
   constexpr int NT = RT < 256 ? 256 : RT, TEAMS = NT / RT;
   __shared__ float red[2][RT / 64];
   __shared__ float sums[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? 512 : 1];
+  constexpr int E = unit_of(DK, HK), U = 8 * C / E;
   constexpr int BYTES = InKind<DK>::kBytes + 2 * InKind<HK>::kBytes;
   constexpr bool DH_AHEAD = C == 1 || BYTES <= 6, KEEP_W = C == 1 || BYTES <= 10, H_AHEAD = KEEP_W;
   const int t = threadIdx.x % RT, team = threadIdx.x / RT;
   const int64_t teams = (int64_t)gridDim.x * TEAMS;
-  const int chunks = (int)(p.cols / 8);
-  float w[C][8], acc[C][8];
-  Raw8<DK> dy[C];
-  Raw8<HK> h[C], dh[C];
+  const int units = (int)(p.cols / E);
+  float w[U][E], acc[U][E];
+  Raw<DK, E> dy[U];
+  Raw<HK, E> h[U], dh[U];
   float rstd = 0.0f;
-  auto load_row = [&](int64_t row, Raw8<DK>(&dy)[C], Raw8<HK>(&h)[C], Raw8<HK>(&dh)[C], float& rstd) {
+  auto load_row = [&](int64_t row, Raw<DK, E>(&dy)[U], Raw<HK, E>(&h)[U], Raw<HK, E>(&dh)[U], float& rstd) {
     rstd = p.rstd[row];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int ch = i * RT + t;
-      if (ch < chunks) {
-        dy[i] = load8<DK, ONCE>(p.dy, row * p.lddy + 8 * ch);
-        if (H_AHEAD) h[i] = load8<HK, ONCE>(p.h, row * p.ldh + 8 * ch);
-        if (DH_AHEAD) dh[i] = load_dh8<HK, ONCE>(p, row, 8 * ch);
+    for (int i = 0; i < U; ++i) {
+      const int c = E * (i * RT + t);
+      if (i * RT + t < units) {
+        dy[i] = load_raw<DK, E, ONCE>(p.dy, row * p.lddy + c);
+        if (H_AHEAD) h[i] = load_raw<HK, E, ONCE>(p.h, row * p.ldh + c);
+        if (DH_AHEAD) dh[i] = load_dh<HK, E, ONCE>(p, row, c);
       }
     }
   };
   int64_t row = (int64_t)blockIdx.x * TEAMS + team;
   if (row < p.rows) load_row(row, dy, h, dh, rstd);
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int ch = i * RT + t;
+  for (int i = 0; i < U; ++i) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
-    if (KEEP_W && ch < chunks) load_w8(p.w, 8 * ch, w[i]);
+    for (int k = 0; k < E; ++k) acc[i][k] = 0.0f;
+    if (KEEP_W && i * RT + t < units) load_w(p.w, E * (i * RT + t), w[i]);
   }
   for (int it = 0; row < p.rows; row += teams, ++it) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int ch = i * RT + t;
-      if (ch < chunks) {
-        if (!KEEP_W) load_w8(p.w, 8 * ch, w[i]);
-        if (!H_AHEAD) h[i] = load8<HK, ONCE>(p.h, row * p.ldh + 8 * ch);
-        if (!DH_AHEAD) dh[i] = load_dh8<HK, ONCE>(p, row, 8 * ch);
-        float g[8], n[8];
-        widen8(dy[i], g);
-        widen8(h[i], n);
+    for (int i = 0; i < U; ++i) {
+      const int c = E * (i * RT + t);
+      if (i * RT + t < units) {
+        if (!KEEP_W) load_w(p.w, c, w[i]);
+        if (!H_AHEAD) h[i] = load_raw<HK, E, ONCE>(p.h, row * p.ldh + c);
+        if (!DH_AHEAD) dh[i] = load_dh<HK, E, ONCE>(p, row, c);
+        float g[E], n[E];
+        widen_raw(dy[i], g);
+        widen_raw(h[i], n);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < E; ++k) {
           n[k] *= rstd;
           s = __builtin_fmaf(g[k] * w[i][k], n[k], s);
           acc[i][k] = __builtin_fmaf(g[k], n[k], acc[i][k]);
         }
       }
     }
-    Raw8<DK> dy1[C];
-    Raw8<HK> h1[C], dh1[C];
+    Raw<DK, E> dy1[U];
+    Raw<HK, E> h1[U], dh1[U];
     float rstd1 = 0.0f;
     const bool more = row + teams < p.rows;
     if (more) load_row(row + teams, dy1, h1, dh1, rstd1);
     // two areas in turn: a wave writes one again only after the other's barrier
     s = row_sum<RT>(s, red[it & 1], t) / (float)p.cols;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int ch = i * RT + t;
-      if (ch < chunks) {
-        if (!KEEP_W) load_w8(p.w, 8 * ch, w[i]);
-        store_dx8<DK, HK, ONCE>(p, dy[i], h[i], dh[i], w[i], rstd, s, row * p.cols + 8 * ch);
+    for (int i = 0; i < U; ++i) {
+      const int c = E * (i * RT + t);
+      if (i * RT + t < units) {
+        if (!KEEP_W) load_w(p.w, c, w[i]);
+        store_dx<ONCE>(p, dy[i], h[i], dh[i], w[i], rstd, s, row * p.cols + c);
       }
     }
     if (more) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
+      for (int i = 0; i < U; ++i) {
         dy[i] = dy1[i];
         if (H_AHEAD) h[i] = h1[i];
         if (DH_AHEAD) dh[i] = dh1[i];
@@ -384,10 +378,12 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
   float* const part = p.ws + (int64_t)blockIdx.x * p.cols;
   if constexpr (TEAMS > 1) {
     static_assert(C == 1 && RT * 8 <= 512, "a team's columns fit its row of sums");
-    if (t < chunks) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sums[team][8 * t + k] = acc[0][k];
-    }
+    for (int i = 0; i < U; ++i)
+      if (i * RT + t < units) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) sums[team][E * (i * RT + t) + k] = acc[i][k];
+      }
     __syncthreads();
     for (int c = threadIdx.x; c < (int)p.cols; c += NT) {
       float v = sums[0][c];
@@ -397,10 +393,8 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int ch = i * RT + t;
-      if (ch < chunks) store8<0>(part, 8 * ch, round8<0>(acc[i]));
-    }
+    for (int i = 0; i < U; ++i)
+      if (i * RT + t < units) store_raw(part, E * (i * RT + t), round_raw<0>(acc[i]));
   }
 }
 
@@ -408,23 +402,23 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
 // twice, the columns' sums by rmsnorm_bwd_cols.
 template <int DK, int HK>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_rows_long(const NormBwdArgs p) {
-  constexpr int RT = 1024;
+  constexpr int RT = 1024, E = unit_of(DK, HK);
   __shared__ float red[RT / 64];
   const int64_t row = blockIdx.x;
-  const int chunks = (int)(p.cols / 8);
+  const int units = (int)(p.cols / E);
   const float rstd = p.rstd[row];
   float s = 0.0f;
-  for (int ch = threadIdx.x; ch < chunks; ch += RT) {
-    float w[8];
-    load_w8(p.w, 8 * ch, w);
-    s = row_part8<DK, HK>(load8<DK>(p.dy, row * p.lddy + 8 * ch), load8<HK>(p.h, row * p.ldh + 8 * ch), w, rstd, s);
+  for (int u = threadIdx.x; u < units; u += RT) {
+    float w[E];
+    load_w(p.w, E * u, w);
+    s = row_part(load_raw<DK, E>(p.dy, row * p.lddy + E * u), load_raw<HK, E>(p.h, row * p.ldh + E * u), w, rstd, s);
   }
   s = row_sum<RT>(s, red, (int)threadIdx.x) / (float)p.cols;
-  for (int ch = threadIdx.x; ch < chunks; ch += RT) {
-    float w[8];
-    load_w8(p.w, 8 * ch, w);
-    store_dx8<DK, HK>(p, load8<DK>(p.dy, row * p.lddy + 8 * ch), load8<HK>(p.h, row * p.ldh + 8 * ch),
-                      load_dh8<HK>(p, row, 8 * ch), w, rstd, s, row * p.cols + 8 * ch);
+  for (int u = threadIdx.x; u < units; u += RT) {
+    float w[E];
+    load_w(p.w, E * u, w);
+    store_dx(p, load_raw<DK, E>(p.dy, row * p.lddy + E * u), load_raw<HK, E>(p.h, row * p.ldh + E * u),
+             load_dh<HK, E>(p, row, E * u), w, rstd, s, row * p.cols + E * u);
   }
 }
 
@@ -444,8 +438,8 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_cols(const NormBwdArgs p, flo
   if (c < p.cols) {
     for (int64_t r = r0 + wave; r < r1; r += 4) {
       float g[8], h[8];
-      widen8(load8<DK>(p.dy, r * p.lddy + c), g);
-      widen8(load8<HK>(p.h, r * p.ldh + c), h);
+      widen_raw(load_raw<DK, 8>(p.dy, r * p.lddy + c), g);
+      widen_raw(load_raw<HK, 8>(p.h, r * p.ldh + c), h);
       const float rstd = p.rstd[r];
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(g[k], h[k] * rstd, acc[k]);

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace dg {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -156,101 +158,128 @@ __device__ __forceinline__ int encode4(v4f v, float s, float inv) {
 // them written nontemporally (ONCE below).
 constexpr int64_t kOnceBytes = 64ll << 20;
 
-// Eight consecutive elements of kind K as loaded (one or two 16-byte words),
-// so that a value waiting for its row's reduction costs 4 registers for 16-bit
-// kinds, not 8.
-template <int K>
-struct Raw8 {
-  v4u w[InKind<K>::kBytes / 2];
+// E (4 or 8) consecutive elements of kind K as loaded, so that a value waiting
+// for its row's reduction costs half a register for 16-bit kinds.
+//
+// A lane takes eight elements at a time where every operand is 16-bit and four
+// where one is FP32 (unit_of), so that it moves 16 bytes of the widest operand
+// in one instruction and neighbouring lanes touch neighbouring pieces: copying
+// 512 MB in pieces of 32 bytes per lane, two instructions each, runs at 4.18
+// TB/s, in single 16-byte pieces at 5.90.
+template <int K, int E>
+struct Raw {
+  static constexpr int W = E * InKind<K>::kBytes / 4;  // words
+  unsigned w[W];
 };
 
+constexpr int unit_of(int k0, int k1) { return k0 == 0 || k1 == 0 ? 4 : 8; }
+
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+
 // p: base of a matrix of kind K; e: index of the first element (the address
-// is 16-byte aligned). ONCE (here and below): nontemporal, for data that is
-// larger than the caches.
-template <int K, bool ONCE = false>
-__device__ __forceinline__ Raw8<K> load8(const void* p, int64_t e) {
-  Raw8<K> r;
-  const v4u* src = reinterpret_cast<const v4u*>(static_cast<const char*>(p) + e * InKind<K>::kBytes);
+// is aligned to the E elements' bytes, up to 16). ONCE (here and below):
+// nontemporal, for data that is larger than the caches.
+template <int K, int E, bool ONCE = false>
+__device__ __forceinline__ Raw<K, E> load_raw(const void* p, int64_t e) {
+  typedef typename std::conditional<Raw<K, E>::W == 2, v2u, v4u>::type V;
+  constexpr int N = sizeof(V) / 4;
+  Raw<K, E> r;
+  const V* src = reinterpret_cast<const V*>(static_cast<const char*>(p) + e * InKind<K>::kBytes);
 #pragma unroll
-  for (int i = 0; i < InKind<K>::kBytes / 2; ++i) {
-    if constexpr (ONCE) r.w[i] = __builtin_nontemporal_load(src + i);
-    else r.w[i] = src[i];
+  for (int i = 0; i < Raw<K, E>::W / N; ++i) {
+    const V v = ONCE ? __builtin_nontemporal_load(src + i) : src[i];
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.w[i * N + k] = v[k];
   }
   return r;
 }
 
-template <int K>
-__device__ __forceinline__ void widen8(const Raw8<K>& r, float (&f)[8]) {
-  const v4f a = widen<K, 0>(r.w[0]);
-  const v4f b = K == 0 ? widen<K, 0>(r.w[InKind<K>::kBytes / 2 - 1]) : widen<K, 1>(r.w[0]);
+template <int K, int E>
+__device__ __forceinline__ void widen_raw(const Raw<K, E>& r, float (&f)[E]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = a[i];
-    f[4 + i] = b[i];
+  for (int q = 0; q < E / 4; ++q) {
+    v4f v;
+    if constexpr (K == 0) v = widen<K, 0>((v4u){r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]});
+    else v = widen<K, 0>((v4u){r.w[2 * q], r.w[2 * q + 1], 0u, 0u});
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[4 * q + i] = v[i];
   }
 }
 
 // FP32 -> kind K, round to nearest even (FP16: past 65504 to infinity).
-template <int K>
-__device__ __forceinline__ Raw8<K> round8(const float (&f)[8]) {
+template <int K, int E>
+__device__ __forceinline__ Raw<K, E> round_raw(const float (&f)[E]) {
   typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-  Raw8<K> r;
+  Raw<K, E> r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (K == 0) {
-      r.w[0][i] = __float_as_uint(f[i]);
-      r.w[InKind<K>::kBytes / 2 - 1][i] = __float_as_uint(f[4 + i]);
-    } else if constexpr (K == 1) {
-      r.w[0][i] = __builtin_bit_cast(unsigned, (v2bf){(__bf16)f[2 * i], (__bf16)f[2 * i + 1]});
-    } else {
-      r.w[0][i] = __builtin_bit_cast(unsigned, (v2h){(_Float16)f[2 * i], (_Float16)f[2 * i + 1]});
-    }
+  for (int i = 0; i < Raw<K, E>::W; ++i) {
+    if constexpr (K == 0) r.w[i] = __float_as_uint(f[i]);
+    else if constexpr (K == 1) r.w[i] = __builtin_bit_cast(unsigned, (v2bf){(__bf16)f[2 * i], (__bf16)f[2 * i + 1]});
+    else r.w[i] = __builtin_bit_cast(unsigned, (v2h){(_Float16)f[2 * i], (_Float16)f[2 * i + 1]});
   }
   return r;
 }
 
-template <int K, bool ONCE = false>
-__device__ __forceinline__ void store8(void* p, int64_t e, const Raw8<K>& r) {
-  v4u* dst = reinterpret_cast<v4u*>(static_cast<char*>(p) + e * InKind<K>::kBytes);
+template <bool ONCE = false, int K, int E>
+__device__ __forceinline__ void store_raw(void* p, int64_t e, const Raw<K, E>& r) {
+  typedef typename std::conditional<Raw<K, E>::W == 2, v2u, v4u>::type V;
+  constexpr int N = sizeof(V) / 4;
+  V* dst = reinterpret_cast<V*>(static_cast<char*>(p) + e * InKind<K>::kBytes);
 #pragma unroll
-  for (int i = 0; i < InKind<K>::kBytes / 2; ++i) {
-    if constexpr (ONCE) __builtin_nontemporal_store(r.w[i], dst + i);
-    else dst[i] = r.w[i];
+  for (int i = 0; i < Raw<K, E>::W / N; ++i) {
+    V v;
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = r.w[i * N + k];
+    if constexpr (ONCE) __builtin_nontemporal_store(v, dst + i);
+    else dst[i] = v;
   }
 }
 
-template <bool ONCE>
-__device__ __forceinline__ void store_codes8(uint8_t* q, v2i codes) {
-  if constexpr (ONCE) __builtin_nontemporal_store(codes, reinterpret_cast<v2i*>(q));
-  else *reinterpret_cast<v2i*>(q) = codes;
-}
-
-// Max over the lanes that share a g-wide segment when a lane holds eight of
-// its elements: g / 8 = 8, 16 or 32 lanes (g the same for the whole launch).
+// Max over the lanes that share a g-wide segment when a lane holds E of its
+// elements: g / E = 8 to 64 lanes (g the same for the whole launch).
+template <int E>
 __device__ __forceinline__ float segment_max(float m, int g) {
   m = group_max<8>(m);
-  if (g >= 128) m = fmaxf(m, dpp_f<0x140>(m));
-  if (g >= 256) m = fmaxf(m, __shfl_xor(m, 16, 64));
+  if (g / E >= 16) m = fmaxf(m, dpp_f<0x140>(m));
+  if (g / E >= 32) m = fmaxf(m, __shfl_xor(m, 16, 64));
+  if (g / E >= 64) m = fmaxf(m, __shfl_xor(m, 32, 64));
   return m;
 }
 
-__device__ __forceinline__ float amax8(const float (&y)[8]) {
-  return fmaxf(amax4((v4f){y[0], y[1], y[2], y[3]}), amax4((v4f){y[4], y[5], y[6], y[7]}));
+template <int E>
+__device__ __forceinline__ float amax_of(const float (&y)[E]) {
+  float m = amax4((v4f){y[0], y[1], y[2], y[3]});
+  if constexpr (E == 8) m = fmaxf(m, amax4((v4f){y[4], y[5], y[6], y[7]}));
+  return m;
 }
 
 __device__ __forceinline__ float format_max(int fmt) { return fmt == 1 ? 57344.0f : 448.0f; }
 
-// Eight codes of y / s (fmt 0 E4M3FN, 1 E5M2, the same for the whole launch);
+// The codes of y / s (fmt 0 E4M3FN, 1 E5M2, the same for the whole launch) to q;
 // inv = 1 / s where recip_ok(s).
-template <int FMT>
-__device__ __forceinline__ v2i encode8_fmt(const float (&y)[8], float s, float inv) {
-  const v4f a = {y[0], y[1], y[2], y[3]}, b = {y[4], y[5], y[6], y[7]};
-  if (recip_ok(s)) return (v2i){encode4<FMT, true>(a, s, inv), encode4<FMT, true>(b, s, inv)};
-  return (v2i){encode4<FMT, false>(a, s, inv), encode4<FMT, false>(b, s, inv)};
+template <int FMT, bool ONCE, int E>
+__device__ __forceinline__ void store_codes_fmt(uint8_t* q, const float (&y)[E], float s, float inv) {
+  int c[E / 4];
+  const bool fast = recip_ok(s);
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    const v4f v = {y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
+    if (fast) c[i] = encode4<FMT, true>(v, s, inv);
+    else c[i] = encode4<FMT, false>(v, s, inv);
+  }
+  if constexpr (E == 8) {
+    if constexpr (ONCE) __builtin_nontemporal_store((v2i){c[0], c[1]}, reinterpret_cast<v2i*>(q));
+    else *reinterpret_cast<v2i*>(q) = (v2i){c[0], c[1]};
+  } else {
+    if constexpr (ONCE) __builtin_nontemporal_store(c[0], reinterpret_cast<int*>(q));
+    else *reinterpret_cast<int*>(q) = c[0];
+  }
 }
 
-__device__ __forceinline__ v2i encode8(const float (&y)[8], float s, float inv, int fmt) {
-  return fmt == 1 ? encode8_fmt<1>(y, s, inv) : encode8_fmt<0>(y, s, inv);
+template <bool ONCE = false, int E>
+__device__ __forceinline__ void store_codes(uint8_t* q, const float (&y)[E], float s, float inv, int fmt) {
+  if (fmt == 1) store_codes_fmt<1, ONCE>(q, y, s, inv);
+  else store_codes_fmt<0, ONCE>(q, y, s, inv);
 }
 
 // Sum over the wave in every lane, in a fixed order: DPP swaps and mirrors
