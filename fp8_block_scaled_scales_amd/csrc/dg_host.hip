@@ -614,10 +614,11 @@ const char* dg_strerror(int code) {
     case DG_EINVAL:
       return "invalid argument (null pointer, bad dimension, K not a multiple of gran, gran not 64/128/256, "
              "sa_rows neither gran nor 1, a format code other than DG_FMT_E4M3/DG_FMT_E5M2, an unknown "
-             "activation or layout, an "
+             "activation, layout or element type, a row pitch shorter than its row, an "
              "output or workspace that overlaps another argument, or a workspace smaller than the plan needs)";
     case DG_EALIGN:
-      return "misaligned pointer (a, b need 16 bytes; sa, sb, bias 4 bytes; out 2 bytes; workspace 256 bytes)";
+      return "misaligned pointer or row pitch (a, b need 16 bytes; sa, sb, bias 4 bytes; out 2 bytes; workspace 256 "
+             "bytes; the norm's and the gradients' matrices and row pitches 16 bytes)";
     case DG_EUNSUPPORTED: return "unsupported device (gfx950 required)";
     case DG_ESCRATCH:
       return "the call's K split needs more workspace than dg_gemm_fp8_noalloc's fixed scratch "

@@ -11,6 +11,10 @@
 // activation and residual type. Rows of any pitch and base keep the 16-byte
 // accesses (global memory takes them at any address; the types below carry
 // the elements' own alignment): only the last few columns go one by one.
+//
+// Bound by HBM at the ends of tiles that all CUs reach together: 8192^3 takes
+// 474.9 us with bias, BF16 residual and pre (268 MB more, 45 us at a copy's
+// rate) and 501.7 with GELU too, where the plain product takes 433.7.
 #pragma once
 
 #include <hip/hip_runtime.h>
