@@ -558,7 +558,8 @@ int epilogue_backward(const void* dout, int dout_type, int64_t lddout, const voi
   if (fmt != DG_FMT_E4M3 && fmt != DG_FMT_E5M2) return DG_EINVAL;
   if (!good_dims(rows, cols) || !good_gran(gran, cols) || (block_rows != gran && block_rows != 1)) return DG_EINVAL;
   if (!good_pitch(lddout, cols) || (pre && !good_pitch(ldpre, cols))) return DG_EINVAL;
-  if (((rows + block_rows - 1) / block_rows) * (cols / gran) > 0x7fffffff) return DG_EINVAL;
+  // a workgroup of up to 1024 threads per g x g block (256 at g = 64) in a grid of less than 2^32 threads
+  if (block_rows != 1 && ((rows + gran - 1) / gran) * (cols / gran) > (gran == 64 ? 0xffffff : 0x3fffff)) return DG_EINVAL;
   const int64_t need = dbias ? dg::epi_bwd_workspace(rows, cols, gran, block_rows) : 0;
   if (ws_bytes < need || (need > 0 && !ws)) return DG_EINVAL;
   const uint64_t ds = kind_size(dout_type);

@@ -23,6 +23,7 @@ struct NormArgs {
   float eps;
   int gran, fmt, xk, rk;
   int gshift, segs;  // log2(gran), cols / gran
+  int64_t row0;      // a launch's first row
 };
 
 struct NormBwdArgs {

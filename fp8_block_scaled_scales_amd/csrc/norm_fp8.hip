@@ -116,7 +116,7 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_quant(const NormA
   constexpr int ROWS = RT < 256 ? 256 / RT : 1;
   __shared__ float red[ROWS][RT / 64];
   const int t = threadIdx.x % RT, team = threadIdx.x / RT;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + team;
+  const int64_t row = p.row0 + (int64_t)blockIdx.x * ROWS + team;
   if (RT == 64 && row >= p.rows) return;  // whole waves, and no barrier follows
   const int units = row < p.rows ? (int)(p.cols / E) : 0;  // a team past the last row only meets the barrier
   Raw<HK, E> h[U];
@@ -148,7 +148,7 @@ template <int XK, int RK>
 __global__ __launch_bounds__(1024) void rmsnorm_quant_long(const NormArgs p) {
   constexpr int HK = RK == kAbsent ? XK : RK, RT = 1024, E = unit_of_norm(XK, RK);
   __shared__ float red[RT / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = p.row0 + blockIdx.x;
   const int units = (int)(p.cols / E);
   float ss = 0.0f;
   for (int u = threadIdx.x; u < units; u += RT) {
@@ -166,17 +166,30 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long(const NormArgs p) {
   }
 }
 
+// One launch, or several where a grid's threads would pass 2^32 - 1; `wg_rows`
+// rows per workgroup of NT threads.
+template <int NT, class K>
+hipError_t launch_by_rows(K kernel, const NormArgs& p, int wg_rows, hipStream_t stream) {
+  const int64_t most = 0xffffffffll / NT;
+  for (int64_t r0 = 0; r0 < p.rows; r0 += most * wg_rows) {
+    NormArgs q = p;
+    q.row0 = r0;
+    const int64_t wgs = std::min<int64_t>(most, (p.rows - r0 + wg_rows - 1) / wg_rows);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(NT), 0, stream, q);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
 template <int XK, int RK, int RT, int C>
 hipError_t launch_rows(const NormArgs& p, hipStream_t stream) {
-  constexpr int ROWS = RT < 256 ? 256 / RT : 1;
-  const dim3 grid((unsigned)((p.rows + ROWS - 1) / ROWS)), block(RT < 256 ? 256 : RT);
+  constexpr int ROWS = RT < 256 ? 256 / RT : 1, NT = RT * ROWS;
   // kOnceBytes: 8192x8192 in BF16 85.6 -> 81.4 us nontemporally, 2622x14976
   // (training) 69.9 -> 59.7, 4000x16384 85.0 -> 78.6; 300x4096 4.3 -> 4.5
   if (p.rows * p.cols * (InKind<XK>::kBytes + (RK == kAbsent ? 0 : InKind<RK % kAbsent>::kBytes)) >= kOnceBytes)
-    hipLaunchKernelGGL((rmsnorm_quant<XK, RK, RT, C, true>), grid, block, 0, stream, p);
-  else
-    hipLaunchKernelGGL((rmsnorm_quant<XK, RK, RT, C, false>), grid, block, 0, stream, p);
-  return hipGetLastError();
+    return launch_by_rows<NT>(rmsnorm_quant<XK, RK, RT, C, true>, p, ROWS, stream);
+  return launch_by_rows<NT>(rmsnorm_quant<XK, RK, RT, C, false>, p, ROWS, stream);
 }
 
 // Threads per row: one chunk each as long as 1024 reach, which leaves the
@@ -193,8 +206,7 @@ hipError_t launch_norm_k(const NormArgs& p, hipStream_t stream) {
   if (p.cols <= 8192) return launch_rows<XK, RK, 1024, 1>(p, stream);
   if (p.cols <= 16384) return launch_rows<XK, RK, 1024, 2>(p, stream);
   if (p.cols <= 32768) return launch_rows<XK, RK, 1024, 4>(p, stream);
-  hipLaunchKernelGGL((rmsnorm_quant_long<XK, RK>), dim3((unsigned)p.rows), dim3(1024), 0, stream, p);
-  return hipGetLastError();
+  return launch_by_rows<1024>(rmsnorm_quant_long<XK, RK>, p, 1, stream);
 }
 
 template <int XK>

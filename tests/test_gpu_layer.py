@@ -568,3 +568,17 @@ def test_offsets_past_32_bits(dg):
     torch.cuda.synchronize()
     dz = x[-n:].cpu().double() * (x[-n:].cpu().double() > 0)
     ref.check_codes(q[-n:].cpu(), s[-n:].cpu(), dz, 1, 128, 0, 2 * ref.U32)
+
+
+def test_norm_of_more_threads_than_a_grid_holds(dg):
+    """2^22 rows of 1024 threads pass 2^32 threads: further rows go into a second launch."""
+    rows, cols, n = (1 << 22) + 3, 4160, 5
+    x = torch.ones(rows, cols, dtype=BF16, device=DEV)
+    x[-n:] = ref.stream(9, n, cols, BF16).to(DEV)
+    w = weight(cols).to(DEV)
+    say("norm of %d rows" % rows)
+    q, s, _ = dg.dg_rmsnorm_quantize_fp8(x, None, w, gran=64)
+    torch.cuda.synchronize()
+    _, _, y = ref.norm(x[-n:].cpu(), None, w.cpu(), 1e-6)
+    ref.check_codes(q[-n:].cpu(), s[-n:].cpu(), y, 1, 64, 0, NORM_REL)
+    assert torch.equal(q[0], q[rows // 2]) and torch.equal(s[0], s[rows - n - 1])

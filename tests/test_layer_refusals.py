@@ -81,6 +81,9 @@ def _epi(dg, dout=X, dk=1, lddout=256, pre=PRE, ldpre=256, act=2, rows=300, cols
     (dict(q=Q + 4), "EALIGN"), (dict(db=DW + 2), "EALIGN"), (dict(s=S + 2), "EALIGN"), (dict(ws=WS + 4), "EALIGN"),
     (dict(dz=PRE), "EINVAL"), (dict(q=X), "EINVAL"), (dict(db=PRE), "EINVAL"), (dict(dz=X, lddout=512), "EINVAL"),
     (dict(rows=4096, ws=X), "EINVAL"), (dict(s=Q), "EINVAL"),
+    # more than 2^22 - 1 blocks of 128, 2^24 - 1 of 64 (addresses spread far enough that nothing overlaps)
+    (dict(rows=1 << 20, cols=1 << 16, lddout=1 << 16, ldpre=1 << 16, nb=1 << 34), "EINVAL"),
+    (dict(rows=1 << 20, cols=1 << 16, lddout=1 << 16, ldpre=1 << 16, g=64, br=64, nb=1 << 36), "EINVAL"),
 ])
 def test_epilogue_backward_refuses(dg, kw, want):
     assert _epi(dg, **kw) == getattr(dg, "DG_" + want)
