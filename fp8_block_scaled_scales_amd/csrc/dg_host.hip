@@ -45,7 +45,7 @@ constexpr int64_t kWsFloats = 4ll << 20;  // 16 MB of partial tiles
 constexpr int64_t kSplitMinSteps = 128;
 constexpr int64_t kSplitMin = 8;
 
-// The same bounds for dg_gemm_fp8_residual. With a transposed operand the
+// kSplitMinSteps for the residual epilogue's form. With a transposed operand the
 // streaming tiles take its K rows in 32-byte pieces at about half the rate, the
 // 64x64 tiles in 64-byte ones, so a split wins earlier: 19x51x12352 TN 25.2 ->
 // 11.9 us, 565x68x10240 TT 19.9 -> 13.5, 47x19x6656 TT 11.0 -> 9.9; 2x453x3840
@@ -294,9 +294,12 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
   if (((uintptr_t)a & 15) || ((uintptr_t)b & 15) || ((uintptr_t)sa & 3) || ((uintptr_t)sb & 3) ||
       ((uintptr_t)out & 1))
     return DG_EALIGN;
+  // The residual epilogue's form; with nothing that the plain forms lack they
+  // run, by their own plan (the same sums and roundings: the same bits).
+  const bool form3 = rs && (rs->res || rs->pre || act > DG_ACT_GELU);
   // A workspace lets few-tile long-K shapes split K; without one nothing does.
   Plan pl = plan(M, N, K, gran, split_ok && (ws_bytes > 0 || use_scratch),
-                 rs ? residual_split_steps(layout) : kSplitMinSteps);
+                 form3 ? residual_split_steps(layout) : kSplitMinSteps);
   if (!pl.e || pl.tiles * pl.ksplit > 0x7fffffff) return DG_EINVAL;
   const int64_t need = workspace_bytes(pl);
   if (ws_bytes > 0 && ws_bytes < need) return DG_EINVAL;
@@ -363,8 +366,6 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
   p.bias = bias;
   p.act = act;
   p.epi = {};
-  // nothing that the plain forms lack: they run (the same product and rounding)
-  const bool form3 = rs && (rs->res || rs->pre || act > DG_ACT_GELU);
   if (form3) {
     p.epi.bias = bias;
     p.epi.res = rs->res;

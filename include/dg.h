@@ -406,9 +406,12 @@ int dg_quantize_fp8_rows_typed(const void* x, int in_type, int64_t rows, int64_t
  *        (from 8192, or from 6144 where an operand is stored transposed) split
  *        K over workgroups; NULL and 0 for no split.
  *
- * The product and pre are dg_gemm_fp8_ws's (without a workspace: its tile
- * choice in every layout), and without res and pre and with one of its three
- * activations the result is that call's, bit for bit. Status codes as dg_gemm_fp8_layout.
+ * Without res and pre and with one of dg_gemm_fp8_ws's three activations the
+ * call is dg_gemm_fp8_ws, bit for bit, with a workspace and without (it then
+ * splits K where that call does, from 16384). Otherwise, without a workspace,
+ * pre is the bits of that call's output for DG_ACT_NONE; where a K split adds
+ * the partial products in another order, z differs from the unsplit one by
+ * the FP32 roundings of its sum. Status codes as dg_gemm_fp8_layout.
  */
 int dg_gemm_fp8_residual(const void* a, const void* b, const float* sa, const float* sb, void* out, int64_t M,
                          int64_t N, int64_t K, int gran, int layout, int sa_rows, int fmt_a, int fmt_b,
@@ -416,7 +419,8 @@ int dg_gemm_fp8_residual(const void* a, const void* b, const float* sa, const fl
                          void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes with which that call splits K for these sizes (0: it does
- * not; DG_EINVAL for sizes it would reject). */
+ * not; DG_EINVAL for sizes it would reject). Without res, pre and the further
+ * activations it needs as many or none. */
 int64_t dg_gemm_fp8_residual_workspace(int64_t M, int64_t N, int64_t K, int gran, int layout);
 
 /*
