@@ -577,8 +577,10 @@ def dg_gemm_fp8_residual(a, b, sa, sb, res=None, out=None, gran: int = 128, layo
     float32, bfloat16 or float16, rows contiguous (any pitch), or None; it may be out
     itself. act: one of the five DG_ACT_* codes. pre: optional [M,N] bfloat16 that
     receives C + bias, for dg_epilogue_backward_fp8. workspace: a uint8 tensor of
-    dg_gemm_fp8_residual_workspace(...) bytes, which only few output tiles with a long K
-    use (allocated when None).
+    dg_gemm_fp8_residual_workspace(...) bytes, with which few output tiles and a long K
+    are split over workgroups: allocated when None, where dg_gemm_fp8_ws does not split;
+    an empty tensor declines the split, so that a row's sums do not depend on the number
+    of output tiles through it.
     """
     if stream is None:
         rc = _binding.gemm_residual(a, b, sa, sb, res, out, gran, layout, gran if sa_rows is None else sa_rows, fmt_a, fmt_b, bias,
