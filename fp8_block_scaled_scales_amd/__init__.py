@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch  # loads the HIP runtime libdg.so binds to
 
@@ -124,13 +125,28 @@ def load_library(path: str):
 
 
 _lib = load_library(LIB_PATH)
+
+
+class _NoBinding:
+    """In place of a _binding that is not there: every call is left to the Python functions, which need libdg.so alone."""
+
+    @staticmethod
+    def _leave(*args):
+        return None
+
+    gemm_residual = rmsnorm_quantize = rmsnorm_backward = epilogue_backward = _leave
+
+
 try:
     from . import _binding  # the short way into the calls that serve a few tokens
 except ImportError as e:
-    raise ImportError("_binding.so is not built for this torch (run fp8_block_scaled_scales_amd.build.build()): %s" % e)
-_binding.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
-    "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward", "dg_rmsnorm_backward_workspace", "dg_epilogue_backward_fp8",
-    "dg_epilogue_backward_workspace", "dg_gemm_fp8_residual", "dg_gemm_fp8_residual_workspace")))
+    warnings.warn("_binding.so is not built for this torch (run fp8_block_scaled_scales_amd.build.build()): calls of a few "
+                  "tokens take some microseconds more (%s)" % e, RuntimeWarning)
+    _binding = _NoBinding
+else:
+    _binding.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
+        "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward", "dg_rmsnorm_backward_workspace", "dg_epilogue_backward_fp8",
+        "dg_epilogue_backward_workspace", "dg_gemm_fp8_residual", "dg_gemm_fp8_residual_workspace")))
 lib = _lib  # raw ctypes handle, for tests that exercise the C ABI directly
 
 
