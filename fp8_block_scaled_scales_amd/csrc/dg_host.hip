@@ -449,6 +449,10 @@ bool clash(const Range (&outs)[NO], const Range (&ins)[NI], int o = -1, int i = 
 
 bool good_dims(int64_t rows, int64_t cols) { return rows > 0 && cols > 0 && rows <= DG_MAX_DIM && cols <= DG_MAX_DIM; }
 bool good_gran(int gran, int64_t cols) { return (gran == 64 || gran == 128 || gran == 256) && cols % gran == 0; }
+// The gradient's g x g blocks: a workgroup of up to 1024 threads each (256 at g = 64) in a grid of less than 2^32 threads.
+bool good_blocks(int64_t rows, int64_t cols, int gran, int block_rows) {
+  return block_rows == 1 || ((rows + gran - 1) / gran) * (cols / gran) <= (gran == 64 ? 0xffffff : 0x3fffff);
+}
 bool misaligned(const void* p, uint64_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
 // rows of 16-byte pieces: the base and the row pitch
 bool misaligned_rows(const void* p, int64_t ld, uint64_t esize) { return p && (misaligned(p, 16) || (ld * esize) % 16); }
@@ -559,8 +563,7 @@ int epilogue_backward(const void* dout, int dout_type, int64_t lddout, const voi
   if (fmt != DG_FMT_E4M3 && fmt != DG_FMT_E5M2) return DG_EINVAL;
   if (!good_dims(rows, cols) || !good_gran(gran, cols) || (block_rows != gran && block_rows != 1)) return DG_EINVAL;
   if (!good_pitch(lddout, cols) || (pre && !good_pitch(ldpre, cols))) return DG_EINVAL;
-  // a workgroup of up to 1024 threads per g x g block (256 at g = 64) in a grid of less than 2^32 threads
-  if (block_rows != 1 && ((rows + gran - 1) / gran) * (cols / gran) > (gran == 64 ? 0xffffff : 0x3fffff)) return DG_EINVAL;
+  if (!good_blocks(rows, cols, gran, block_rows)) return DG_EINVAL;
   const int64_t need = dbias ? dg::epi_bwd_workspace(rows, cols, gran, block_rows) : 0;
   if (ws_bytes < need || (need > 0 && !ws)) return DG_EINVAL;
   const uint64_t ds = kind_size(dout_type);
@@ -774,7 +777,8 @@ int dg_rmsnorm_backward(const void* dy, int dy_type, int64_t lddy, const void* h
 }
 
 int64_t dg_epilogue_backward_workspace(int64_t rows, int64_t cols, int gran, int block_rows) {
-  return good_dims(rows, cols) && good_gran(gran, cols) && (block_rows == gran || block_rows == 1)
+  return good_dims(rows, cols) && good_gran(gran, cols) && (block_rows == gran || block_rows == 1) &&
+                 good_blocks(rows, cols, gran, block_rows)
              ? dg::epi_bwd_workspace(rows, cols, gran, block_rows)
              : (int64_t)DG_EINVAL;
 }

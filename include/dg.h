@@ -499,7 +499,7 @@ int64_t dg_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  *   q      FP8 codes out, [rows][cols], 8-byte aligned.
  *   scales FP32 out, [ceil(rows/block_rows)][cols/gran]; with gran x gran blocks
  *          at most 2^24 - 1 blocks of 64 or 2^22 - 1 of 128 or 256 (DG_EINVAL
- *          beyond: 6.8e10 elements).
+ *          beyond: 6.8e10 elements, at gran 256 2.7e11).
  *   workspace  at least dg_epilogue_backward_workspace bytes with dbias (NULL
  *          where that is 0, and without dbias), 16-byte aligned; as above.
  *
