@@ -210,6 +210,9 @@ Plan plan(int64_t M, int64_t N, int64_t K, int sgran, bool split_ok, int64_t spl
   return p;
 }
 
+// Whether a plan has an entry and a grid that a launch takes.
+bool runs(const Plan& p) { return p.e && p.tiles * p.ksplit <= 0x7fffffff; }
+
 // Workspace bytes of a plan: none without a K split.
 int64_t workspace_bytes(const Plan& p) {
   if (p.ksplit <= 1) return 0;
@@ -300,7 +303,7 @@ int gemm(const void* a, const void* b, const float* sa, const float* sb, void* o
   // A workspace lets few-tile long-K shapes split K; without one nothing does.
   Plan pl = plan(M, N, K, gran, split_ok && (ws_bytes > 0 || use_scratch),
                  form3 ? residual_split_steps(layout) : kSplitMinSteps);
-  if (!pl.e || pl.tiles * pl.ksplit > 0x7fffffff) return DG_EINVAL;
+  if (!runs(pl)) return DG_EINVAL;
   const int64_t need = workspace_bytes(pl);
   if (ws_bytes > 0 && ws_bytes < need) return DG_EINVAL;
   if (use_scratch && need > kScratchBytes) return DG_ESCRATCH;
@@ -645,7 +648,7 @@ int query(int64_t M, int64_t N, int64_t K, int gran, int layout, bool split_ok, 
   if (rc != DG_OK) return rc;
   if ((rc = validate_layout(M, N, layout)) != DG_OK) return rc;
   const Plan p = plan(M, N, K, gran, split_ok);
-  if (!p.e || p.tiles * p.ksplit > 0x7fffffff) return DG_EINVAL;
+  if (!runs(p)) return DG_EINVAL;
   info->kernel_id = p.e->id;
   info->bm = p.e->bm;
   info->bn = p.e->bn;
@@ -755,7 +758,8 @@ int dg_gemm_fp8_residual(const void* a, const void* b, const float* sa, const fl
 
 int64_t dg_gemm_fp8_residual_workspace(int64_t M, int64_t N, int64_t K, int gran, int layout) {
   if (validate(M, N, K, gran) != DG_OK || validate_layout(M, N, layout) != DG_OK) return DG_EINVAL;
-  return workspace_bytes(plan(M, N, K, gran, true, residual_split_steps(layout)));
+  const Plan p = plan(M, N, K, gran, true, residual_split_steps(layout));
+  return runs(p) ? workspace_bytes(p) : (int64_t)DG_EINVAL;
 }
 
 int dg_rmsnorm_quantize_fp8(const void* x, int x_type, int64_t ldx, const void* res, int res_type, int64_t ldres,
