@@ -550,6 +550,7 @@ int rmsnorm_backward(const void* dy, int dy_type, int64_t lddy, const void* h, i
   p.lddh = lddh;
   p.dk = dy_type;
   p.hk = h_type;
+  p.row0 = 0;
   if (log_enabled())
     std::fprintf(stderr, "dg_rmsnorm_backward rows=%lld cols=%lld dy=%d h=%d dh=%d workspace %lld\n", (long long)rows,
                  (long long)cols, dy_type, h_type, dh ? 1 : 0, (long long)need);

@@ -37,6 +37,7 @@ struct NormBwdArgs {
   float* ws;       // partial column sums (norm_bwd_workspace bytes)
   int64_t rows, cols, lddy, ldh, lddh;
   int dk, hk;
+  int64_t row0;  // a launch's first row, where rows take several
 };
 
 struct EpiBwdArgs {

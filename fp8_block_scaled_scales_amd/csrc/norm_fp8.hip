@@ -168,11 +168,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_long(const NormArgs p) {
 
 // One launch, or several where a grid's threads would pass 2^32 - 1; `wg_rows`
 // rows per workgroup of NT threads.
-template <int NT, class K>
-hipError_t launch_by_rows(K kernel, const NormArgs& p, int wg_rows, hipStream_t stream) {
+template <int NT, class K, class Args>
+hipError_t launch_by_rows(K kernel, const Args& p, int wg_rows, hipStream_t stream) {
   const int64_t most = 0xffffffffll / NT;
   for (int64_t r0 = 0; r0 < p.rows; r0 += most * wg_rows) {
-    NormArgs q = p;
+    Args q = p;
     q.row0 = r0;
     const int64_t wgs = std::min<int64_t>(most, (p.rows - r0 + wg_rows - 1) / wg_rows);
     hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(NT), 0, stream, q);
@@ -420,7 +420,7 @@ template <int DK, int HK>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_rows_long(const NormBwdArgs p) {
   constexpr int RT = 1024, E = unit_of(DK, HK);
   __shared__ float red[RT / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = p.row0 + blockIdx.x;
   const int units = (int)(p.cols / E);
   const float rstd = p.rstd[row];
   float s = 0.0f;
@@ -539,7 +539,8 @@ hipError_t launch_norm_bwd_k(const NormBwdArgs& p, hipStream_t stream) {
     const int64_t col_groups = (p.cols + 511) / 512;
     hipLaunchKernelGGL((rmsnorm_bwd_cols<DK, HK>), dim3((unsigned)(col_groups * b.partial)), dim3(256), 0, stream, q, q.ws,
                        (int)col_groups, (int)b.partial);
-    hipLaunchKernelGGL((rmsnorm_bwd_rows_long<DK, HK>), dim3((unsigned)p.rows), dim3(1024), 0, stream, q);
+    const hipError_t err = launch_by_rows<1024>(rmsnorm_bwd_rows_long<DK, HK>, q, 1, stream);
+    if (err != hipSuccess) return err;
   } else if (b.rt == 64) {
     launch_bwd<DK, HK, 64, 1>(q, b, stream);
   } else if (b.rt == 256) {
