@@ -72,7 +72,7 @@ class MLP:
 
 def reference(w1, b1, w2, b2, norm_weight, x, residual, dout):
     """The same step in FP32 on unquantised weights: out and the six gradients."""
-    leaves = [t.float().requires_grad_() for t in (x, norm_weight, w1, b1, w2, b2)]
+    leaves = [t.detach().float().clone().requires_grad_() for t in (x, norm_weight, w1, b1, w2, b2)]
     xf, nw, w1f, b1f, w2f, b2f = leaves
     h = xf + residual.float()
     y = h * torch.rsqrt(h.square().mean(1, keepdim=True) + EPS) * nw

@@ -106,6 +106,14 @@ def test_bounds_find_planted_mistakes(tokens, hidden, ffn):
     assert "out" in failures(got, want, x, residual, dout)
 
 
+def test_reference_leaves_its_arguments_alone():
+    import mlp_step
+
+    weights, x, residual, dout = mlp_step.inputs(8, 16, 24, device="cpu")
+    mlp_step.reference(*weights, x, residual, dout)
+    assert not any(t.requires_grad for t in weights + (x, residual, dout))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("tokens,hidden,ffn", [(128, 256, 512), (384, 1024, 640), (1024, 512, 2048), (2176, 768, 1920)])
 def test_step(tokens, hidden, ffn):
