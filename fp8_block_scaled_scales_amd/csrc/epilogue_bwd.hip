@@ -139,9 +139,11 @@ __global__ __launch_bounds__(NT) void epi_bwd_blocks(const EpiBwdArgs p, float* 
     for (int k = 0; k < E; ++k) sums[rsub][cl * E + k] = acc[k];
   }
   __syncthreads();
+  DG_STEP_SYNC_WG();
   amax = red[0];
 #pragma unroll
   for (int w = 1; w < NT / 64; ++w) amax = fmaxf(amax, red[w]);
+  DG_STEP_SYNC_WG();
   const float s = block_scale(amax, format_max(p.fmt));
   const float inv = 1.0f / s;
   if (t == 0) p.scales[block] = s;
@@ -204,6 +206,7 @@ __global__ __launch_bounds__(64 * NW) void epi_bwd_rows(const EpiBwdArgs p, floa
 #pragma unroll
   for (int k = 0; k < E; ++k) sums[wave][lane * E + k] = acc[k];
   __syncthreads();
+  DG_STEP_SYNC_WG();
   const int64_t col = (int64_t)cg * COLS + threadIdx.x;
   if (threadIdx.x < COLS && col < p.cols) {
     float v = sums[0][threadIdx.x];

@@ -50,11 +50,13 @@ template <int RT>
 __device__ __forceinline__ float row_sum(float v, float* red, int t) {
   v = wave_sum(v);
   if constexpr (RT > 64) {
+    DG_STEP_SYNC_WG();
     if ((t & 63) == 0) red[t >> 6] = v;
     __syncthreads();
     v = red[0];
 #pragma unroll
     for (int i = 1; i < RT / 64; ++i) v += red[i];
+    DG_STEP_SYNC_WG();
   }
   return v;
 }
@@ -401,6 +403,7 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rmsnorm_bwd_many(const No
         for (int k = 0; k < E; ++k) sums[team][E * (i * RT + t) + k] = acc[i][k];
       }
     __syncthreads();
+    DG_STEP_SYNC_WG();
     for (int c = threadIdx.x; c < (int)p.cols; c += NT) {
       float v = sums[0][c];
 #pragma unroll
@@ -464,6 +467,7 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_cols(const NormBwdArgs p, flo
 #pragma unroll
   for (int k = 0; k < 8; ++k) red[wave][lane * 8 + k] = acc[k];
   __syncthreads();
+  DG_STEP_SYNC_WG();
   for (int i = threadIdx.x; i < 512; i += 256) {
     const int64_t col = (int64_t)cg * 512 + i;
     if (col < p.cols) out[rr * p.cols + col] = ((red[0][i] + red[1][i]) + red[2][i]) + red[3][i];
@@ -586,6 +590,7 @@ __global__ __launch_bounds__(1024) void column_sum(const float* __restrict__ par
     if ((threadIdx.x & 63) < CL) red[wave][cl * 4 + k] = s[k];
   }
   __syncthreads();
+  DG_STEP_SYNC_WG();
   if (threadIdx.x < 4 * CL) {
     float v = red[0][threadIdx.x];
 #pragma unroll

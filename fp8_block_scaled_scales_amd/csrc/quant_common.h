@@ -8,6 +8,8 @@
 
 #include <type_traits>
 
+#include "race_check.h"
+
 namespace dg {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -300,16 +302,20 @@ __device__ __forceinline__ float wave_sum(float v) {
 template <int RL, int CL>
 __device__ __forceinline__ void column_sums_of_lanes(const float (&acc)[8], float (&red)[RL][8 * CL], float* out) {
   const int cl = threadIdx.x % CL, rl = threadIdx.x / CL;
+  DG_STEP_SYNC_WG();
 #pragma unroll
   for (int k = 0; k < 8; ++k) red[rl][cl * 8 + k] = acc[k];
   __syncthreads();
+  DG_STEP_SYNC_WG();
   const int c = threadIdx.x % (8 * CL), g = threadIdx.x / (8 * CL);
   float v = red[g * 8][c];
 #pragma unroll
   for (int i = 1; i < 8; ++i) v += red[g * 8 + i][c];
   __syncthreads();
+  DG_STEP_SYNC_WG();
   red[g][c] = v;
   __syncthreads();
+  DG_STEP_SYNC_WG();
   if (g == 0) {
 #pragma unroll 16
     for (int i = 1; i < RL / 8; ++i) v += red[i][c];
