@@ -155,11 +155,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
     bcol[j] = hb && col < N ? bias[col] : 0.0f;
   }
 
-  // Form 3: the first pass's residual, ahead of the copies too.
+  // Form 3: the first pass's residual, ahead of the copies too (with a K split
+  // the second kernel reads it).
   using Tile = ResidualTile<BN, BN + 4, NT, WM, WTM, 32>;
   const Tile tile{epi, m0, n0, M, N};
   RawResidual<8> res[2][Tile::ITS];
-  if constexpr (EPI == 3) tile.load(0, res[0]);
+  if constexpr (EPI == 3) {
+    if (!SPLIT || ksplit == 1) tile.load(0, res[0]);
+  }
 
   // Prologue: fill STAGES-1 ring slots.
 #pragma unroll
