@@ -35,7 +35,10 @@ __device__ __forceinline__ float act_fn(float z) {
 // e = exp(-a^2/2) the value at -a is e * (P(t)/2 - a / sqrt(2 pi)), where
 // P(t) e is erfc(a / sqrt 2) by Abramowitz and Stegun 7.1.26 (the polynomial of
 // erf_as7126), t = 1 / (1 + 0.3275911 a / sqrt 2): one exponential serves both
-// terms, and both tails go to exactly 0 and 1. Absolute error below 1e-7.
+// terms, and both tails go to exactly 0 and 1. Absolute error: the polynomial's
+// 7e-8, and up to 2.2e-7 from the roundings of t and of its alternating terms near
+// t = 1 (2.9e-7 together at |z| = 0.067 with an exact reciprocal and exp2; 2.3e-7
+// measured over every BF16 z).
 //
 // SiLU and the tanh form are z p(v), p = sigmoid(v), with v = z and v = 2u;
 // their derivative p + z p (1 - p) v' is 1 minus its value at -z too. With
