@@ -88,27 +88,35 @@ TRAFFIC = {
     "decode_m64_n4096_k7168": {"src": "86e89fe55db16f3c", "bytes": 33667236},
 }
 
-# Sources that make up each workload's kernel: its class's device code, the
-# shared device header, the argument header and the host dispatch.
-_COMMON_SOURCES = ("gemm_common.h", "gemm_fp8_nt.h", "dg_host.hip")
+# What makes up each workload's kernel: the unit that compiles its class, the
+# host dispatch and, by their #include lines, the headers of the device code.
 KERNEL_SOURCES = {
-    "decode_m64_n4096_k7168": ("gemm_fp8_stream.hip",) + _COMMON_SOURCES,
-    "square8192": ("gemm_fp8_big.h", "gemm_fp8_nt_big.hip") + _COMMON_SOURCES,
-    "prefill_m4096_n7168_k2048": ("gemm_fp8_big.h", "gemm_fp8_nt_big.hip") + _COMMON_SOURCES,
-    "longk_m2000_n4000_k16384_g64": ("gemm_fp8_big.h", "gemm_fp8_nt_big.hip") + _COMMON_SOURCES,
+    "decode_m64_n4096_k7168": ("gemm_fp8_stream.hip", "dg_host.hip"),
+    "square8192": ("gemm_fp8_nt_big.hip", "dg_host.hip"),
+    "prefill_m4096_n7168_k2048": ("gemm_fp8_nt_big.hip", "dg_host.hip"),
+    "longk_m2000_n4000_k16384_g64": ("gemm_fp8_nt_big.hip", "dg_host.hip"),
 }
 
 
 def kernel_source_hash(workload: str) -> str | None:
     import hashlib
+    import re
 
     names = KERNEL_SOURCES.get(workload)
     if names is None:
         return None
-    h = hashlib.sha256()
-    for name in names:
+    texts, todo = {}, list(names)
+    while todo:
+        name = todo.pop()
+        if name in texts:
+            continue
         with open(os.path.join(ROOT, "fp8_block_scaled_scales_amd", "csrc", name), "rb") as f:
-            h.update(f.read())
+            texts[name] = f.read()
+        if name != "dg_host.hip":
+            todo += re.findall(r'#include "(\w+\.h)"', texts[name].decode())
+    h = hashlib.sha256()
+    for name in sorted(texts):
+        h.update(texts[name])
     return h.hexdigest()[:16]
 
 
