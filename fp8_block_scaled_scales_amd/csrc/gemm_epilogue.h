@@ -14,7 +14,8 @@
 //
 // Bound by HBM at the ends of tiles that all CUs reach together: 8192^3 takes
 // 474.9 us with bias, BF16 residual and pre (268 MB more, 45 us at a copy's
-// rate) and 501.7 with GELU too, where the plain product takes 433.7.
+// rate) and 501.7 with GELU too, where the plain product takes 433.7 (one set of
+// operands; with three sets in turn 520 and 454).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -18,12 +18,12 @@
 // of x and of the residual alike).
 //
 // Both are bound by HBM: 8 to 12 operations per element against 3 (BF16 without a
-// residual) to 17 bytes (FP32 with residual and y). A row stays in registers between its reduction and its use, so each
-// input is read once: 8192 x 8192 in BF16 takes 98 us forward with y (606 MB,
-// 6.2 TB/s) and 90 us backward (537 MB, 5.9 TB/s, the addition of the partial
-// rows included), 2000 x 16384 with an FP32 stream 62.6 (5.8 TB/s) and 88.2 us
-// (5.2 TB/s), where a copy reaches 5.9 TB/s; one row of 7168 takes 3.0 us, 64
-// rows backward 3.4 us.
+// residual) to 17 bytes (FP32 with residual and y). A row stays in registers
+// between its reduction and its use, so each input is read once: 8192 x 8192 in
+// BF16 takes 98 us forward with y (606 MB, 6.2 TB/s) and 90 us backward (537 MB,
+// 5.9 TB/s, the addition of the partial rows included), 2000 x 16384 with an FP32
+// stream 62.6 (5.8 TB/s) and 88.2 us (5.2 TB/s), where a copy reaches 5.9 TB/s;
+// one row of 7168 takes 3.0 us, 64 rows backward 3.4 us.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -70,6 +70,15 @@ __device__ __forceinline__ float amax_load(v4u w) {
   }
 }
 
+// A block's factor: amax / fmax (correctly rounded), or 1.0 where that is
+// zero: an all-zero block, or one whose amax is so small that the quotient
+// underflows (no factor of zero to divide by; 1.0 encodes its values, all
+// below fmax * 2^-150, under 2^-134, as zeros).
+__device__ __forceinline__ float block_scale(float amax, float fmax) {
+  const float s = amax / fmax;
+  return s > 0.0f ? s : 1.0f;
+}
+
 // Division by a block's scale s, rounded as the correctly rounded FP32 divide
 // rounds it, without a divide per element. inv = RN(1/s) is computed once per
 // block (a correctly rounded divide); per element q0 = RN(x * inv) lies within
@@ -86,15 +95,6 @@ __device__ __forceinline__ float amax_load(v4u w) {
 // wrong in its last bits, but every such value is far below half the smallest
 // FP8 subnormal and encodes to a signed zero either way; the sign is x's (an
 // input -0 gives -0, where the corrections alone would give +0).
-// A block's factor: amax / fmax (correctly rounded), or 1.0 where that is
-// zero: an all-zero block, or one whose amax is so small that the quotient
-// underflows (no factor of zero to divide by; 1.0 encodes its values, all
-// below fmax * 2^-150, under 2^-134, as zeros).
-__device__ __forceinline__ float block_scale(float amax, float fmax) {
-  const float s = amax / fmax;
-  return s > 0.0f ? s : 1.0f;
-}
-
 __device__ __forceinline__ bool recip_ok(float s) { return s >= 0x1p-120f && s <= 0x1p120f; }
 
 __device__ __forceinline__ float div_by_scale(float x, float s, float inv) {
