@@ -42,6 +42,7 @@ DG_ACT_RELU = 1
 DG_ACT_GELU = 2
 DG_ACT_SILU = 3
 DG_ACT_GELU_TANH = 4
+DG_MAX_GROUPS = 1024  # experts or adapters of one call
 DG_MAX_DIM = (1 << 24) - 256  # largest M, N or K (and quantiser rows, cols) the library accepts
 
 
@@ -117,6 +118,29 @@ def load_library(path: str):
                                              vp, vp, vp, vp, i64, vp]
     lib.dg_epilogue_backward_workspace.restype = i64
     lib.dg_epilogue_backward_workspace.argtypes = [i64, i64, ctypes.c_int, ctypes.c_int]
+    i32 = ctypes.c_int
+    lib.dg_route_sort.restype = i32
+    lib.dg_route_sort.argtypes = [vp, i32, i64, i32, i32, i32, vp, vp, vp, i64, vp, i64, vp]
+    lib.dg_route_rows.restype = i64
+    lib.dg_route_rows.argtypes = [i64, i32, i32, i32]
+    lib.dg_route_sort_workspace.restype = i64
+    lib.dg_route_sort_workspace.argtypes = [i64, i32, i32]
+    lib.dg_route_quantize_fp8.restype = i32
+    lib.dg_route_quantize_fp8.argtypes = [vp, kind, i64, i64, i64, i32, vp, vp, i64, vp, i32, i32, fmt, vp, vp, vp, i64, vp]
+    lib.dg_route_quantize_workspace.restype = i64
+    lib.dg_route_quantize_workspace.argtypes = [i64, i64, i32, i64, i32, i32]
+    lib.dg_route_combine.restype = i32
+    lib.dg_route_combine.argtypes = [vp, kind, i64, i64, i64, i64, i32, vp, vp, vp, i64, vp, kind, vp]
+    lib.dg_route_weight_grad.restype = i32
+    lib.dg_route_weight_grad.argtypes = [vp, kind, i64, vp, kind, i64, i64, i64, i64, i32, vp, vp, vp]
+    lib.dg_gemm_fp8_grouped.restype = i32
+    lib.dg_gemm_fp8_grouped.argtypes = [vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, i32, i32, i32, fmt, fmt, act, vp, vp]
+    lib.dg_gemm_fp8_grouped_wgrad.restype = i32
+    lib.dg_gemm_fp8_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, i32, fmt, fmt, vp]
+    lib.dg_lora.restype = i32
+    lib.dg_lora.argtypes = [vp, kind, i64, i64, i64, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp, i64, vp, kind, vp, i64, vp]
+    lib.dg_lora_workspace.restype = i64
+    lib.dg_lora_workspace.argtypes = [i64, i64, i64, i32, i32]
     lib.dg_strerror.restype = ctypes.c_char_p
     lib.dg_strerror.argtypes = [ctypes.c_int]
     lib.dg_version.restype = ctypes.c_int
@@ -135,6 +159,7 @@ class _NoBinding:
         return None
 
     gemm_residual = rmsnorm_quantize = rmsnorm_backward = epilogue_backward = _leave
+    route_sort = route_quantize = route_combine = route_weight_grad = gemm_grouped = grouped_wgrad = lora = _leave
 
 
 try:
@@ -147,6 +172,9 @@ else:
     _binding.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
         "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward", "dg_rmsnorm_backward_workspace", "dg_epilogue_backward_fp8",
         "dg_epilogue_backward_workspace", "dg_gemm_fp8_residual", "dg_gemm_fp8_residual_workspace")))
+    _binding.bind_route(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
+        "dg_route_sort", "dg_route_sort_workspace", "dg_route_quantize_fp8", "dg_route_quantize_workspace", "dg_route_combine",
+        "dg_route_weight_grad", "dg_gemm_fp8_grouped", "dg_gemm_fp8_grouped_wgrad", "dg_lora", "dg_lora_workspace")))
 lib = _lib  # raw ctypes handle, for tests that exercise the C ABI directly
 
 
@@ -778,6 +806,320 @@ def dg_epilogue_backward_workspace(rows: int, cols: int, gran: int = 128, block_
     return n
 
 
+# ---- layers whose weights each row chooses: experts and adapters ------------
+
+_I32 = (torch.int32,)
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+_ACTS = (DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU, DG_ACT_SILU, DG_ACT_GELU_TANH)
+
+
+def _count(n, name):
+    """A size the library computed, or the error it answered with."""
+    if n < 0:
+        _raise(n, name)
+    return n
+
+
+def _groups(offsets, dev):
+    """The number of groups that an offsets array is for."""
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 2 <= offsets.shape[0] <= DG_MAX_GROUPS + 1:
+        raise ValueError("offsets must be a 1-D tensor of 2 to DG_MAX_GROUPS + 1 entries")
+    _check(offsets, "offsets", _I32, (offsets.shape[0],), dev)
+    return offsets.shape[0] - 1
+
+
+def dg_route_sort(ids, groups: int, align: int = 1, offsets=None, position=None, slot=None, workspace=None, stream=None):
+    """(offsets, position, slot): the stable sort of every token's choices by group, as the calls below take it.
+
+    ids: [tokens, k] int32 or int64 (torch.topk's, say); a value outside 0 .. groups - 1
+    takes the choice out. align: every group starts at a multiple of it (1, or gran for
+    calls with gran x gran factors). offsets [groups + 1] int32: group e has the sorted
+    rows offsets[e] .. offsets[e + 1] - 1. position [tokens, k] int32: each choice's row
+    (-1: none). slot int32, at least dg_route_rows(...) long: each row's choice t * k + j
+    (-1: a row between groups, -2: behind the last). Nothing is copied to the host.
+    workspace: a uint8 tensor of dg_route_sort_workspace(...) bytes (allocated when None).
+    """
+    if stream is None:
+        rc = _binding.route_sort(ids, groups, align, offsets, position, slot, workspace)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_route_sort")
+            return offsets, position, slot
+    tokens, k = shape = _matrix(ids, "ids")
+    dev = ids.device
+    _check(ids, "ids", tuple(_ID_BYTES), shape, dev)
+    least = _count(_lib.dg_route_rows(tokens, k, groups, align), "dg_route_sort")
+    if slot is not None and (slot.dim() != 1 or slot.shape[0] < least):
+        raise ValueError("slot must be 1-D with at least dg_route_rows(...) = %d entries" % least)
+    rows = least if slot is None else slot.shape[0]
+    offsets = _out(offsets, "offsets", _I32, (groups + 1,), dev, stream)
+    position = _out(position, "position", _I32, shape, dev, stream)
+    slot = _out(slot, "slot", _I32, (rows,), dev, stream)
+    need = _lib.dg_route_sort_workspace(tokens, k, groups)
+    ws = _workspace(workspace, need, dev, stream) if need > 0 else None
+    _launch(_lib.dg_route_sort, "dg_route_sort", dev, stream, ids.data_ptr(), _ID_BYTES[ids.dtype], tokens, k, groups, align,
+            offsets.data_ptr(), position.data_ptr(), slot.data_ptr(), rows, _ptr(ws), ws.numel() if need > 0 else 0)
+    return offsets, position, slot
+
+
+def dg_route_rows(tokens: int, k: int, groups: int, align: int = 1) -> int:
+    """Sorted rows that hold any routing of tokens x k choices among groups."""
+    return _count(_lib.dg_route_rows(tokens, k, groups, align), "dg_route_rows")
+
+
+def dg_route_sort_workspace(tokens: int, k: int, groups: int) -> int:
+    """Workspace bytes of dg_route_sort."""
+    return _count(_lib.dg_route_sort_workspace(tokens, k, groups), "dg_route_sort_workspace")
+
+
+def _routing(x, position, slot, weights, dev):
+    """Checks (x, position, slot, weights) of a call on [tokens, k] choices; (tokens, cols, k, rows)."""
+    tokens, cols = _matrix(x, "x")
+    k = _matrix(position, "position")[1]
+    _check(position, "position", _I32, (tokens, k), dev)
+    rows = 0
+    if slot is not None:
+        rows = slot.numel() if isinstance(slot, torch.Tensor) else 0
+        _check(slot, "slot", _I32, (rows,), dev)
+    if weights is not None:
+        _check(weights, "weights", _F32, (tokens, k), dev)
+    return tokens, cols, k, rows
+
+
+def dg_route_quantize_fp8(x, position, slot, weights=None, gran: int = 128, block_rows: int = 1, fmt: int = DG_FMT_E4M3,
+                          q=None, scales=None, workspace=None, stream=None):
+    """(q, scales): the tokens x as FP8 rows in sorted order, each multiplied by its choice's weight where they are given.
+
+    The dispatch to the experts; with the combine's weights on the gradient of its output,
+    the combine's gradient. x: [tokens, cols] float32, bfloat16 or float16 (any row pitch).
+    position, slot: from dg_route_sort. weights: [tokens, k] float32. block_rows: 1 (a
+    factor per row and segment) or gran (gran x gran blocks of sorted rows, which serve
+    the weights' gradient too). q: [rows, cols] uint8 holding fmt's codes, or that float8
+    dtype; scales: [ceil(rows/block_rows), cols/gran]. Rows between groups get codes of
+    zero, rows behind the last group are left as they were. workspace: a uint8 tensor of
+    dg_route_quantize_workspace(...) bytes (allocated when None).
+    """
+    if stream is None:
+        rc = _binding.route_quantize(x, position, slot, weights, gran, block_rows, fmt, q, scales, workspace)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_route_quantize_fp8")
+            return q, scales
+    _matrix(x, "x")
+    dev = x.device
+    tokens, cols, k, rows = _routing(x, position, slot, weights, dev)
+    if gran not in _GRANS or cols % gran or not rows:
+        raise ValueError("slot must have rows, and gran must be 64, 128 or 256 and divide cols")
+    if block_rows not in (gran, 1):
+        raise ValueError("block_rows must be gran (g x g blocks) or 1 (per-row factors)")
+    if fmt not in _FP8_OF:
+        raise ValueError("fmt must be DG_FMT_E4M3 or DG_FMT_E5M2")
+    ldx = _rows(x, "x", _IN_OF, (tokens, cols), dev)
+    q = _out(q, "q", _FP8_OF[fmt], (rows, cols), dev, stream)
+    scales = _out(scales, "scales", _F32, ((rows + block_rows - 1) // block_rows, cols // gran), dev, stream)
+    need = _lib.dg_route_quantize_workspace(tokens, cols, k, rows, gran, block_rows)
+    ws = _workspace(workspace, need, dev, stream) if need > 0 else None
+    _launch(_lib.dg_route_quantize_fp8, "dg_route_quantize_fp8", dev, stream, x.data_ptr(), _IN_OF[x.dtype], ldx, tokens, cols,
+            k, position.data_ptr(), slot.data_ptr(), rows, _ptr(weights), gran, block_rows, fmt, q.data_ptr(),
+            scales.data_ptr(), _ptr(ws), ws.numel() if need > 0 else 0)
+    return q, scales
+
+
+def dg_route_quantize_workspace(tokens: int, cols: int, k: int, rows: int, gran: int = 128, block_rows: int = 1) -> int:
+    """Workspace bytes of dg_route_quantize_fp8."""
+    return _count(_lib.dg_route_quantize_workspace(tokens, cols, k, rows, gran, block_rows), "dg_route_quantize_workspace")
+
+
+def dg_route_combine(y, position, weights=None, res=None, out=None, stream=None):
+    """out[t] = res[t] + sum over j of weights[t, j] * y[position[t, j]], in float32, rounded once.
+
+    y: [rows, cols] float32, bfloat16 or float16, position: [tokens, k] int32 (choices
+    without a row add nothing), weights: [tokens, k] float32 or None (1 each: the
+    dispatch's gradient), res: [tokens, cols] of out's type or None; it may be out. out's
+    type: any of the three, by default res's or y's. Rows of y and res may have a pitch.
+    """
+    if stream is None:
+        rc = _binding.route_combine(y, position, weights, res, out)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_route_combine")
+            return out
+    rows, cols = _matrix(y, "y")
+    tokens, k = _matrix(position, "position")
+    dev = y.device
+    if not rows or not tokens or not k or cols % 8 or not cols:
+        raise ValueError("y must have rows, and columns in a multiple of 8; position must have entries")
+    _check(position, "position", _I32, (tokens, k), dev)
+    if weights is not None:
+        _check(weights, "weights", _F32, (tokens, k), dev)
+    ldy = _rows(y, "y", _IN_OF, (rows, cols), dev)
+    kinds = (res.dtype,) if res is not None else (out.dtype,) if isinstance(out, torch.Tensor) else (y.dtype,)
+    ldres = 0 if res is None else _rows(res, "res", tuple(_IN_OF), (tokens, cols), dev)
+    if kinds[0] not in _IN_OF:
+        raise ValueError("out must be float32, bfloat16 or float16")
+    out = _out(out, "out", kinds, (tokens, cols), dev, stream)
+    _launch(_lib.dg_route_combine, "dg_route_combine", dev, stream, y.data_ptr(), _IN_OF[y.dtype], ldy, rows, tokens, cols, k,
+            position.data_ptr(), _ptr(weights), _ptr(res), ldres, out.data_ptr(), _IN_OF[out.dtype])
+    return out
+
+
+def dg_route_weight_grad(dout, y, position, dweights=None, stream=None):
+    """dweights[t, j] = the dot product of dout[t] and y[position[t, j]] in float32: the gradient of the combine's weights.
+
+    dout: [tokens, cols], y: [rows, cols], each float32, bfloat16 or float16 (any row
+    pitch); position: [tokens, k] int32; choices without a row get 0.
+    """
+    if stream is None:
+        rc = _binding.route_weight_grad(dout, y, position, dweights)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_route_weight_grad")
+            return dweights
+    tokens, cols = _matrix(dout, "dout")
+    rows = _matrix(y, "y")[0]
+    dev = dout.device
+    k = _matrix(position, "position")[1]
+    if not rows or not tokens or not k or cols % 8 or not cols:
+        raise ValueError("dout and y must have rows, and columns in a multiple of 8; position must have entries")
+    _check(position, "position", _I32, (tokens, k), dev)
+    ldd = _rows(dout, "dout", _IN_OF, (tokens, cols), dev)
+    ldy = _rows(y, "y", _IN_OF, (rows, cols), dev)
+    dweights = _out(dweights, "dweights", _F32, (tokens, k), dev, stream)
+    _launch(_lib.dg_route_weight_grad, "dg_route_weight_grad", dev, stream, dout.data_ptr(), _IN_OF[dout.dtype], ldd,
+            y.data_ptr(), _IN_OF[y.dtype], ldy, rows, tokens, cols, k, position.data_ptr(), dweights.data_ptr())
+    return dweights
+
+
+def dg_gemm_fp8_grouped(a, b, sa, sb, offsets, out=None, gran: int = 128, layout: int = DG_LAYOUT_NT,
+                        sa_rows: int | None = None, fmt_a: int = DG_FMT_E4M3, fmt_b: int = DG_FMT_E4M3,
+                        act: int = DG_ACT_NONE, pre=None, stream=None):
+    """out[r] = bf16(act(a[r] B_e^T)) for the rows r of group e, every group with its own block-scaled B.
+
+    a: [rows, K]; b: [groups, N, K] (DG_LAYOUT_NT) or [groups, K, N] (DG_LAYOUT_NN, the
+    gradient of the rows); sa: [rows, K/gran] with sa_rows = 1, or [ceil(rows/gran),
+    K/gran] with sa_rows = gran (the default; every group then starts at a multiple of
+    gran); sb: [groups, ceil(N/gran), K/gran]; offsets: from dg_route_sort. act: any
+    DG_ACT_* code; pre: optional [rows, N] bfloat16 that receives the product before it,
+    for dg_epilogue_backward_fp8. Rows behind the last group are left as they were.
+    """
+    sa_rows = gran if sa_rows is None else sa_rows
+    if stream is None:
+        rc = _binding.gemm_grouped(a, b, sa, sb, offsets, out, gran, layout, sa_rows, fmt_a, fmt_b, act, pre)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_gemm_fp8_grouped")
+            return out
+    rows, K = _matrix(a, "a")
+    dev = a.device
+    groups = _groups(offsets, dev)
+    if layout not in (DG_LAYOUT_NT, DG_LAYOUT_NN):
+        raise ValueError("layout must be DG_LAYOUT_NT or _NN")
+    if not isinstance(b, torch.Tensor) or b.dim() != 3:
+        raise ValueError("b must be a 3-D tensor")
+    N = b.shape[2] if layout else b.shape[1]
+    if gran not in _GRANS or K % gran or not rows or not N or not K:
+        raise ValueError("a and b must have entries, and gran must be 64, 128 or 256 and divide K")
+    if sa_rows not in (gran, 1):
+        raise ValueError("sa_rows must be gran (g x g blocks) or 1 (per-row factors)")
+    if fmt_a not in _FP8_OF or fmt_b not in _FP8_OF:
+        raise ValueError("formats must be DG_FMT_E4M3 or DG_FMT_E5M2")
+    if act not in _ACTS:
+        raise ValueError("act must be one of the DG_ACT_* codes")
+    _check(a, "a", _FP8_OF[fmt_a], (rows, K), dev)
+    _check(b, "b", _FP8_OF[fmt_b], (groups, K, N) if layout else (groups, N, K), dev)
+    _check(sa, "sa", _F32, ((rows + sa_rows - 1) // sa_rows, K // gran), dev)
+    _check(sb, "sb", _F32, (groups, (N + gran - 1) // gran, K // gran), dev)
+    if pre is not None:
+        _check(pre, "pre", _BF16, (rows, N), dev)
+    out = _out(out, "out", _BF16, (rows, N), dev, stream)
+    _launch(_lib.dg_gemm_fp8_grouped, "dg_gemm_fp8_grouped", dev, stream, a.data_ptr(), b.data_ptr(), sa.data_ptr(),
+            sb.data_ptr(), offsets.data_ptr(), groups, out.data_ptr(), rows, N, K, gran, layout, sa_rows, fmt_a, fmt_b, act,
+            _ptr(pre))
+    return out
+
+
+def dg_gemm_fp8_grouped_wgrad(a, b, sa, sb, offsets, out=None, gran: int = 128, fmt_a: int = DG_FMT_E5M2,
+                              fmt_b: int = DG_FMT_E4M3, stream=None):
+    """out[e] = bf16(A_e^T B_e) over the rows of group e: the gradient of every group's weights.
+
+    a: [rows, M] codes (the gradient of the product's output, E5M2 by default), b:
+    [rows, N] (the product's input), sa: [rows/gran, M/gran] and sb: [rows/gran, N/gran]
+    as the quantisers leave their gran x gran blocks; offsets from dg_route_sort with
+    align a multiple of gran. out: [groups, M, N] bfloat16; zeros for a group without rows.
+    """
+    if stream is None:
+        rc = _binding.grouped_wgrad(a, b, sa, sb, offsets, out, gran, fmt_a, fmt_b)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_gemm_fp8_grouped_wgrad")
+            return out
+    rows, M = _matrix(a, "a")
+    N = _matrix(b, "b")[1]
+    dev = a.device
+    groups = _groups(offsets, dev)
+    if gran not in _GRANS or rows % gran or M % gran or N % gran or not rows or not M or not N:
+        raise ValueError("gran must be 64, 128 or 256 and divide rows and the columns of a and b")
+    if fmt_a not in _FP8_OF or fmt_b not in _FP8_OF:
+        raise ValueError("formats must be DG_FMT_E4M3 or DG_FMT_E5M2")
+    _check(a, "a", _FP8_OF[fmt_a], (rows, M), dev)
+    _check(b, "b", _FP8_OF[fmt_b], (rows, N), dev)
+    _check(sa, "sa", _F32, (rows // gran, M // gran), dev)
+    _check(sb, "sb", _F32, (rows // gran, N // gran), dev)
+    out = _out(out, "out", _BF16, (groups, M, N), dev, stream)
+    _launch(_lib.dg_gemm_fp8_grouped_wgrad, "dg_gemm_fp8_grouped_wgrad", dev, stream, a.data_ptr(), b.data_ptr(), sa.data_ptr(),
+            sb.data_ptr(), offsets.data_ptr(), groups, out.data_ptr(), rows, M, N, gran, fmt_a, fmt_b)
+    return out
+
+
+def dg_lora(x, a, b, offsets, position, slot, scale=None, base=None, out=None, workspace=None, stream=None):
+    """out[t] = base[t] + scale[l] * (x[t] A_l^T) B_l^T, l the adapter of row t; base alone where it has none.
+
+    x: [tokens, K] bfloat16 or float16 (any row pitch); a: [adapters, rank, K] and b:
+    [adapters, N, rank] of its type, rank a multiple of 8 up to 128; scale: [adapters]
+    float32 or None. offsets, position, slot: dg_route_sort(adapter_of_row[:, None],
+    adapters), once for all projections of a step. base: [tokens, N] float32, bfloat16 or
+    float16 (any row pitch), the shared projection's output, or None (zero); out, of its
+    type (x's without base), may be base. workspace: a uint8 tensor of
+    dg_lora_workspace(...) bytes (allocated when None).
+    """
+    if stream is None:
+        rc = _binding.lora(x, a, b, offsets, position, slot, scale, base, out, workspace)
+        if rc is not None:
+            if rc:
+                _raise(rc, "dg_lora")
+            return out
+    tokens, K = _matrix(x, "x")
+    dev = x.device
+    kinds = (torch.bfloat16, torch.float16)
+    ldx = _rows(x, "x", kinds, (tokens, K), dev)
+    groups = _groups(offsets, dev)
+    if not isinstance(a, torch.Tensor) or not isinstance(b, torch.Tensor) or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a and b must be 3-D tensors")
+    rank, N = a.shape[1], b.shape[1]
+    _check(a, "a", (x.dtype,), (groups, rank, K), dev)
+    _check(b, "b", (x.dtype,), (groups, N, rank), dev)
+    need = _count(_lib.dg_lora_workspace(tokens, K, N, rank, groups), "dg_lora")
+    _check(position, "position", _I32, (tokens, 1), dev)
+    _check(slot, "slot", _I32, (tokens,), dev)
+    if scale is not None:
+        _check(scale, "scale", _F32, (groups,), dev)
+    ldbase = 0 if base is None else _rows(base, "base", tuple(_IN_OF), (tokens, N), dev)
+    kind = base.dtype if base is not None else out.dtype if isinstance(out, torch.Tensor) else x.dtype
+    if kind not in _IN_OF:
+        raise ValueError("out must be float32, bfloat16 or float16")
+    out = _out(out, "out", (kind,), (tokens, N), dev, stream)
+    ws = _workspace(workspace, need, dev, stream)
+    _launch(_lib.dg_lora, "dg_lora", dev, stream, x.data_ptr(), _IN_OF[x.dtype], ldx, tokens, K, a.data_ptr(), b.data_ptr(),
+            _ptr(scale), N, rank, groups, offsets.data_ptr(), position.data_ptr(), slot.data_ptr(), _ptr(base), ldbase,
+            out.data_ptr(), _IN_OF[kind], ws.data_ptr(), ws.numel())
+    return out
+
+
+def dg_lora_workspace(tokens: int, K: int, N: int, rank: int, adapters: int) -> int:
+    """Workspace bytes of dg_lora."""
+    return _count(_lib.dg_lora_workspace(tokens, K, N, rank, adapters), "dg_lora_workspace")
+
+
 __all__ = ["dg_gemm_fp8_nt", "dg_gemm_fp8_nt_fmt", "dg_gemm_fp8_nt_epi", "dg_gemm_fp8_nt_ex", "dg_gemm_fp8_layout",
            "dg_gemm_fp8_ws", "dg_workspace", "dg_gemm_fp8_noalloc", "dg_noalloc_scratch_bytes", "DG_ESCRATCH",
            "DG_LAYOUT_NT", "DG_LAYOUT_NN", "DG_LAYOUT_TT", "DG_LAYOUT_TN", "DG_ACT_NONE",
@@ -786,5 +1128,8 @@ __all__ = ["dg_gemm_fp8_nt", "dg_gemm_fp8_nt_fmt", "dg_gemm_fp8_nt_epi", "dg_gem
            "dg_query_tile", "dg_strerror", "dg_version", "DGError", "DGArgumentError", "DG_OK", "DG_EINVAL",
            "dg_gemm_fp8_residual", "dg_gemm_fp8_residual_workspace", "dg_rmsnorm_quantize_fp8", "dg_rmsnorm_backward",
            "dg_rmsnorm_backward_workspace",
+           "dg_route_sort", "dg_route_rows", "dg_route_sort_workspace", "dg_route_quantize_fp8", "dg_route_quantize_workspace",
+           "dg_route_combine", "dg_route_weight_grad", "dg_gemm_fp8_grouped", "dg_gemm_fp8_grouped_wgrad", "dg_lora",
+           "dg_lora_workspace", "DG_MAX_GROUPS",
            "dg_epilogue_backward_fp8", "dg_epilogue_backward_workspace", "DG_ACT_SILU", "DG_ACT_GELU_TANH",
            "DG_EALIGN", "DG_EUNSUPPORTED", "DG_ELAUNCH", "DG_FMT_E4M3", "DG_FMT_E5M2", "DG_MAX_DIM", "LIB_PATH"]

@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libdg.so")
 SOURCES = ["gemm_fp8_big_layouts_rowa.hip", "gemm_fp8_big_layouts.hip", "gemm_fp8_residual.hip",
            "gemm_fp8_residual_big_rowa.hip", "gemm_fp8_residual_big.hip", "gemm_fp8_stream.hip",
            "gemm_fp8_layouts_rowa.hip", "gemm_fp8_layouts.hip", "gemm_fp8_nt_big.hip", "gemm_fp8_nt.hip",
-           "epilogue_bwd.hip", "norm_fp8.hip", "quant_fp8.hip", "dg_host.hip"]
+           "gemm_fp8_grouped_big.hip", "gemm_fp8_grouped.hip", "gemm_fp8_grouped_wgrad.hip", "epilogue_bwd.hip", "norm_fp8.hip",
+           "lora.hip", "route.hip", "quant_fp8.hip", "dg_host.hip", "route_host.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -16,8 +16,11 @@
 
 #include "../../include/dg.h"
 #include "gemm_fp8_nt.h"
+#include "host_checks.h"
 #include "layer_ops.h"
 #include "quant_fp8.h"
+
+using namespace dg;
 
 namespace {
 
@@ -79,16 +82,7 @@ void find_scratch(int dev) {
   g_scratch[dev] = g_scratch_err[dev] == hipSuccess ? p : nullptr;
 }
 
-thread_local hipError_t t_last_hip = hipSuccess;
 thread_local char t_msg[256];
-
-bool log_enabled() {
-  static const bool on = [] {
-    const char* e = std::getenv("DG_LOG");
-    return e && e[0] == '1';
-  }();
-  return on;
-}
 
 void check_device(int dev) {
   hipDeviceProp_t prop;
@@ -136,11 +130,6 @@ struct Plan {
 // DG_FORCE_TILE=<kernel id>, read at every call, replaces the choice when
 // that entry has the call's granularity (tuning, benchmarking and tests; a
 // split-K entry then runs with one split unless the call has a workspace).
-int forced_tile() {
-  const char* e = std::getenv("DG_FORCE_TILE");
-  return e ? std::atoi(e) : -1;
-}
-
 int64_t splits_for(const dg::KernelEntry* e, int64_t tiles, int64_t nsteps) {
   int64_t ks = (256 + tiles / 2) / tiles;
   ks = std::min<int64_t>(std::min<int64_t>(ks, kMaxSplit), nsteps / 4);
@@ -219,8 +208,27 @@ int64_t workspace_bytes(const Plan& p) {
   return p.tiles * p.ksplit * p.e->bm * p.e->bn * (int64_t)sizeof(float);
 }
 
+}  // namespace
+
+namespace dg {
+
+thread_local hipError_t t_last_hip = hipSuccess;
+
+bool log_enabled() {
+  static const bool on = [] {
+    const char* e = std::getenv("DG_LOG");
+    return e && e[0] == '1';
+  }();
+  return on;
+}
+
+int forced_tile() {
+  const char* e = std::getenv("DG_FORCE_TILE");
+  return e ? std::atoi(e) : -1;
+}
+
 // One-time per-device check; returns DG_OK, DG_EUNSUPPORTED or DG_ELAUNCH.
-int device_ready(int* dev_out = nullptr) {
+int device_ready(int* dev_out) {
   int dev = 0;
   if ((t_last_hip = hipGetDevice(&dev)) != hipSuccess) return DG_ELAUNCH;
   if (dev < 0 || dev >= kMaxDevices) return DG_EUNSUPPORTED;
@@ -229,7 +237,7 @@ int device_ready(int* dev_out = nullptr) {
   return g_dev_status[dev];
 }
 
-}  // namespace
+}  // namespace dg
 
 namespace {
 
@@ -245,13 +253,6 @@ int validate_layout(int64_t M, int64_t N, int layout) {
   return DG_OK;
 }
 
-// Whether the byte ranges [p, p + n) and [q, q + m) share a byte (empty
-// ranges share none).
-bool overlaps(const void* p, uint64_t n, const void* q, uint64_t m) {
-  const uintptr_t x = (uintptr_t)p, y = (uintptr_t)q;
-  return n && m && x < y + m && y < x + n;
-}
-
 // The residual epilogue's own arguments (dg_gemm_fp8_residual).
 struct Residual {
   const void* res;
@@ -259,18 +260,6 @@ struct Residual {
   int64_t ldres;
   void* pre;
 };
-
-// Bytes from the first element of a [rows][cols] matrix of row pitch ld to the
-// end of its last.
-uint64_t extent(int64_t rows, int64_t cols, int64_t ld, uint64_t esize) {
-  return esize * ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols);
-}
-
-bool known_kind(int type) { return type == DG_IN_F32 || type == DG_IN_BF16 || type == DG_IN_F16; }
-uint64_t kind_size(int type) { return type == DG_IN_F32 ? 4 : 2; }
-
-// A row pitch of an input: at least the row, at most DG_MAX_DIM.
-bool good_pitch(int64_t ld, int64_t cols) { return ld >= cols && ld <= DG_MAX_DIM; }
 
 // split_ok: few-tile long-K shapes may split K over workgroups, through ws (the
 // caller's, ws_bytes long; none when ws_bytes is 0) or, with use_scratch,
@@ -430,35 +419,10 @@ int quantize(const void* x, int in, int64_t rows, int64_t cols, int gran, int bl
   return t_last_hip == hipSuccess ? DG_OK : DG_ELAUNCH;
 }
 
-// A range of device memory an argument takes; none when p is null.
-struct Range {
-  const void* p;
-  uint64_t n;
-};
-
-// Whether any output overlaps an input or another output, but for the one pair
-// (output `o`, input `i`) that may be the same memory (o < 0: no pair).
-template <int NO, int NI>
-bool clash(const Range (&outs)[NO], const Range (&ins)[NI], int o = -1, int i = -1) {
-  for (int x = 0; x < NO; ++x) {
-    if (!outs[x].p) continue;
-    for (int y = 0; y < NI; ++y)
-      if (ins[y].p && !(x == o && y == i) && overlaps(outs[x].p, outs[x].n, ins[y].p, ins[y].n)) return true;
-    for (int y = 0; y < x; ++y)
-      if (outs[y].p && overlaps(outs[x].p, outs[x].n, outs[y].p, outs[y].n)) return true;
-  }
-  return false;
-}
-
-bool good_dims(int64_t rows, int64_t cols) { return rows > 0 && cols > 0 && rows <= DG_MAX_DIM && cols <= DG_MAX_DIM; }
-bool good_gran(int gran, int64_t cols) { return (gran == 64 || gran == 128 || gran == 256) && cols % gran == 0; }
 // The gradient's g x g blocks: a workgroup of up to 1024 threads each (256 at g = 64) in a grid of less than 2^32 threads.
 bool good_blocks(int64_t rows, int64_t cols, int gran, int block_rows) {
   return block_rows == 1 || ((rows + gran - 1) / gran) * (cols / gran) <= (gran == 64 ? 0xffffff : 0x3fffff);
 }
-bool misaligned(const void* p, uint64_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
-// rows of 16-byte pieces: the base and the row pitch
-bool misaligned_rows(const void* p, int64_t ld, uint64_t esize) { return p && (misaligned(p, 16) || (ld * esize) % 16); }
 
 int rmsnorm_quantize(const void* x, int x_type, int64_t ldx, const void* res, int res_type, int64_t ldres,
                      const float* w, float eps, int64_t rows, int64_t cols, int gran, int fmt, void* h, void* y,

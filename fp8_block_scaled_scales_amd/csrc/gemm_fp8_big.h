@@ -65,6 +65,7 @@
 
 #include "gemm_common.h"
 #include "gemm_fp8_nt.h"
+#include "gemm_groups.h"
 
 namespace dg {
 
@@ -114,12 +115,17 @@ struct Acc<64, WTM, WTN> {
 // length; B transposed on the 256- and 128-wide tiles). A transposed tile is
 // staged as its 128 K rows and read with the transposing LDS read (frag_tr16
 // / frag_tr in gemm_common.h); the K order inside a fragment is the NT order.
-template <int G, int BN, int WM, int GROUP_M, int FMT, int EPI, bool ROWA, int LAYOUT>
+// GRP: NoGroups, or the groups of rows that cut M (RowGroups, B and sb then
+// [groups] of one product's) or K (DepthGroups, LAYOUT 3: out [groups][M][N],
+// and sa and sb as the quantisers leave the stored matrices' factors,
+// [K/sg][M/sg] and [K/sg][N/sg]).
+template <int G, int BN, int WM, int GROUP_M, int FMT, int EPI, bool ROWA, int LAYOUT, class GRP>
 __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict__ a, const uint8_t* __restrict__ b,
                                                       const float* __restrict__ sa, const float* __restrict__ sb,
                                                       uint16_t* __restrict__ out, int M, int N, int K, int tiles_m,
                                                       int tiles_n, int vec_store, int sshift,
-                                                      const float* __restrict__ bias, int relu, const EpiArgs epi) {
+                                                      const float* __restrict__ bias, int relu, EpiArgs epi,
+                                                      const GRP groups) {
   static_assert(G == 64 || G == 128, "granularity");
   constexpr int WN = NW / WM;
   constexpr int WTM = BM / WM, WTN = BN / WN;
@@ -145,7 +151,18 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
   const int grp = wave >> 2;  // copy-issue group: one wave per SIMD in each
 
   int ks, tmi, tni;
-  map_tile<GROUP_M>(tiles_m, tiles_n, ks, tmi, tni);
+  if constexpr (GRP::kKind == 0) {
+    map_tile<GROUP_M>(tiles_m, tiles_n, ks, tmi, tni);
+  } else {
+    GroupTile t;
+    bool live;
+    if constexpr (GRP::kKind == 1) live = find_tile<BM, GROUP_M>(groups, tiles_n, t);
+    else live = find_tile<GROUP_M>(groups, tiles_m, tiles_n, t);
+    if (!live) return;
+    tmi = t.tm;
+    tni = t.tn;
+    enter_group<GRP>(t, G << sshift, ROWA, a, b, sa, sb, out, epi, M, N, K);
+  }
   const int m0 = tmi * BM, n0 = tni * BN;
 
   const uint32_t uK = (uint32_t)K;
@@ -162,10 +179,13 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
   // blocks of rows wr0 and wr0 + 64, one B block.
   const int wr0 = m0 + wm * WTM, wc0 = n0 + wn * WTN;
   const int lastm = (M - 1) / sg, lastn = (N - 1) / sg;
-  const float* const sa0 = sa + (int64_t)min(wr0 / sg, lastm) * nks;
-  const float* const sa1 = sa + (int64_t)min((wr0 + 64) / sg, lastm) * nks;
+  // with DepthGroups a block's factors of successive segments lie a row of factors apart
+  constexpr bool DEPTH = GRP::kKind == 2;
+  const int64_t sap = DEPTH ? lastm + 1 : 1, sbp = DEPTH ? lastn + 1 : 1, sar = DEPTH ? 1 : nks;
+  const float* const sa0 = sa + (int64_t)min(wr0 / sg, lastm) * sar;
+  const float* const sa1 = sa + (int64_t)min((wr0 + 64) / sg, lastm) * sar;
   const int bn0 = wc0 / sg;
-  const float* const sb0 = sb + (int64_t)min(bn0, lastn) * nks;
+  const float* const sb0 = sb + (int64_t)min(bn0, lastn) * sar;
 
   Acc<G, WTM, WTN> acc;
   if constexpr (G == 128) {
@@ -232,7 +252,7 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
   RawResidual<8> res[2][Tile::ITS];
   if constexpr (EPI == 3 && EARLY) tile.load(0, res[0]);
 
-  issue_step(0);
+  if (!DEPTH || nsteps > 0) issue_step(0);
 
   for (int s = 0; s < nsteps; ++s) {
     DG_WAIT_VMCNT(0);  // this wave's part of step s has landed
@@ -287,8 +307,8 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
       constexpr int NJ = WTN / 16, SLOTS = (WTM / 16) * NJ, DSLOT = SLOTS / 4;
       const int r16 = lane & 15, q = lane >> 4;
       const int ksc = s >> sshift;
-      const float a_s = ROWA ? 0.0f : sa0[ksc];
-      const float sbv0 = sb0[ksc];
+      const float a_s = ROWA ? 0.0f : sa0[ksc * sap];
+      const float sbv0 = sb0[ksc * sbp];
       const float sc0 = a_s * sbv0;
       // ROWA: factors of rows 16i + 4q .. +3 of the wave tile, read one row block ahead
       const float* const srow = scl + wm * WTM + 4 * q;
@@ -343,8 +363,8 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
         const int kb = 2 * s + h;
         issue_next(h);
         if (kb < nkb) {  // K % 128 == 64: the last step holds one segment
-          const float sbv = sb0[kb];
-          const float f0 = ROWA ? 0.0f : sa0[kb] * sbv, f1 = ROWA ? 0.0f : sa1[kb] * sbv;
+          const float sbv = sb0[kb * sbp];
+          const float f0 = ROWA ? 0.0f : sa0[kb * sap] * sbv, f1 = ROWA ? 0.0f : sa1[kb * sap] * sbv;
           // ROWA: factors of rows 32i + 8(v/4) + 4*h2 + v%4, read with the row
           // block's first MFMA
           const float* const srow = scl + h * BM + wm * WTM + 4 * h2;
@@ -502,10 +522,33 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
 template <int G, int BN, int WM, int FMT, int EPI, bool ROWA, int LAYOUT>
 hipError_t launch_fa(const GemmArgs& p, hipStream_t stream) {
   const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((gemm_fp8_nt_big<G, BN, WM, 4, FMT, EPI, ROWA, LAYOUT>), dim3(tiles_m * tiles_n), dim3(NT), 0, stream, p.a,
-                     p.b, p.sa, p.sb, p.out, (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.vec_store, p.sshift,
-                     p.bias, p.act == 1 ? 1 : 0, p.epi);
+  hipLaunchKernelGGL((gemm_fp8_nt_big<G, BN, WM, 4, FMT, EPI, ROWA, LAYOUT, NoGroups>), dim3(tiles_m * tiles_n), dim3(NT), 0, stream,
+                     p.a, p.b, p.sa, p.sb, p.out, (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.vec_store, p.sshift,
+                     p.bias, p.act == 1 ? 1 : 0, p.epi, NoGroups{});
   return hipGetLastError();
+}
+
+// The products of groups: p.M rows in all for RowGroups (the residual's epilogue
+// form), p.K for DepthGroups; `grid` workgroups.
+template <int G, int BN, int WM, int FMT, bool ROWA, int LAYOUT, class GRP>
+hipError_t launch_groups_f(const GemmArgs& p, const GRP& g, int64_t grid, hipStream_t stream) {
+  const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
+  constexpr int EPI = GRP::kKind == 1 ? 3 : 0;
+  hipLaunchKernelGGL((gemm_fp8_nt_big<G, BN, WM, 4, FMT, EPI, ROWA, LAYOUT, GRP>), dim3((unsigned)grid), dim3(NT), 0, stream, p.a, p.b,
+                     p.sa, p.sb, p.out, (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.vec_store, p.sshift, nullptr, 0,
+                     p.epi, g);
+  return hipGetLastError();
+}
+
+template <int G, int BN, int WM, bool ROWA, int LAYOUT, class GRP>
+hipError_t launch_groups(const GemmArgs& p, const GRP& g, int64_t grid, hipStream_t stream) {
+  switch (p.fmt) {
+    case 0: return launch_groups_f<G, BN, WM, 0, ROWA, LAYOUT>(p, g, grid, stream);
+    case 1: return launch_groups_f<G, BN, WM, 1, ROWA, LAYOUT>(p, g, grid, stream);
+    case 2: return launch_groups_f<G, BN, WM, 2, ROWA, LAYOUT>(p, g, grid, stream);
+    case 3: return launch_groups_f<G, BN, WM, 3, ROWA, LAYOUT>(p, g, grid, stream);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 // RS selects the A factor forms compiled: 0 both, chosen by p.rowa (the NT

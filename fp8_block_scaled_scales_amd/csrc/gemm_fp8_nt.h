@@ -76,6 +76,15 @@ hipError_t launch_residual(int id, const GemmArgs& p, hipStream_t stream);
 hipError_t launch_residual_big(int id, const GemmArgs& p, hipStream_t stream);
 hipError_t launch_residual_big_rowa(int id, const GemmArgs& p, hipStream_t stream);
 
+// Products over groups of rows (gemm_groups.h) on the tile of table entry `id`,
+// `grid` workgroups: layouts 0 and 1 (every entry), and the weights' gradient
+// (the 128x128 and 256x256 entries, 0, 1, 4 and 5).
+struct RowGroups;
+struct DepthGroups;
+hipError_t launch_grouped(int id, const GemmArgs& p, const RowGroups& g, int64_t grid, hipStream_t stream);
+hipError_t launch_grouped_big(int id, const GemmArgs& p, const RowGroups& g, int64_t grid, hipStream_t stream);
+hipError_t launch_grouped_wgrad(int id, const GemmArgs& p, const DepthGroups& g, int64_t grid, hipStream_t stream);
+
 extern KernelEntry kTable[];
 extern const int kTableSize;
 

@@ -43,6 +43,7 @@
 
 #include "gemm_common.h"
 #include "gemm_fp8_nt.h"
+#include "gemm_groups.h"
 
 namespace dg {
 
@@ -93,8 +94,9 @@ __device__ __forceinline__ v8i frag(const uint8_t* slab, int row, int c0) {
 // G: K segment contracted before each promotion; scale blocks sg = G << sshift
 // (g = 256 runs the G = 128 kernel with one factor per two segments). FMT bit
 // 0: A is E5M2 (else E4M3), bit 1: B is E5M2. ROWA: A's factors are per row,
-// sa is [M][K/sg]. LAYOUT bit 1: A stored [K,M]; bit 0: B stored [K,N].
-template <int G, int FMT, int EPI, bool ROWA, int LAYOUT>
+// sa is [M][K/sg]. LAYOUT bit 1: A stored [K,M]; bit 0: B stored [K,N]. GRP:
+// NoGroups or RowGroups, as gemm_fp8_nt_big's.
+template <int G, int FMT, int EPI, bool ROWA, int LAYOUT, class GRP>
 __global__ __launch_bounds__(64 * NW) void gemm_fp8_stream(const uint8_t* __restrict__ a,
                                                               const uint8_t* __restrict__ b,
                                                               const float* __restrict__ sa,
@@ -102,7 +104,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_fp8_stream(const uint8_t* __rest
                                                               uint16_t* __restrict__ out, int M, int N, int K,
                                                               int tiles_m, int tiles_n, int sshift,
                                                               const float* __restrict__ bias, int relu,
-                                                              const EpiArgs epi) {
+                                                              EpiArgs epi, const GRP groups) {
   static_assert(G == 64 || G == 128, "granularity");
   constexpr bool TA = (LAYOUT & 2) != 0, TB = (LAYOUT & 1) != 0;
   using R = Ring<ROWA>;
@@ -112,7 +114,15 @@ __global__ __launch_bounds__(64 * NW) void gemm_fp8_stream(const uint8_t* __rest
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int ks, tmi, tni;
-  map_tile<2>(tiles_m, tiles_n, ks, tmi, tni);
+  if constexpr (GRP::kKind == 0) {
+    map_tile<2>(tiles_m, tiles_n, ks, tmi, tni);
+  } else {
+    GroupTile t;
+    if (!find_tile<BM, 2>(groups, tiles_n, t)) return;
+    tmi = t.tm;
+    tni = t.tn;
+    enter_group<GRP>(t, G << sshift, ROWA, a, b, sa, sb, out, epi, M, N, K);
+  }
   const int m0 = tmi * BM, n0 = tni * BN;
   const uint32_t uK = (uint32_t)K;
   // NT operands: one descriptor over the tile's rows for the whole K
@@ -330,10 +340,30 @@ __global__ __launch_bounds__(64 * NW) void gemm_fp8_stream(const uint8_t* __rest
 template <int G, int FMT, int EPI, bool ROWA, int LAYOUT>
 hipError_t launch_fa(const GemmArgs& p, hipStream_t stream) {
   const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((gemm_fp8_stream<G, FMT, EPI, ROWA, LAYOUT>), dim3(tiles_m * tiles_n), dim3(64 * NW), 0, stream,
+  hipLaunchKernelGGL((gemm_fp8_stream<G, FMT, EPI, ROWA, LAYOUT, NoGroups>), dim3(tiles_m * tiles_n), dim3(64 * NW), 0, stream,
                      p.a, p.b, p.sa, p.sb, p.out, (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.sshift, p.bias,
-                     p.act == 1 ? 1 : 0, p.epi);
+                     p.act == 1 ? 1 : 0, p.epi, NoGroups{});
   return hipGetLastError();
+}
+
+// The products of groups of rows on the same tile (see big::launch_groups).
+template <int G, int FMT, bool ROWA, int LAYOUT>
+hipError_t launch_groups_f(const GemmArgs& p, const RowGroups& g, int64_t grid, hipStream_t stream) {
+  const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
+  hipLaunchKernelGGL((gemm_fp8_stream<G, FMT, 3, ROWA, LAYOUT, RowGroups>), dim3((unsigned)grid), dim3(64 * NW), 0, stream, p.a, p.b,
+                     p.sa, p.sb, p.out, (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.sshift, nullptr, 0, p.epi, g);
+  return hipGetLastError();
+}
+
+template <int G, bool ROWA, int LAYOUT>
+hipError_t launch_groups(const GemmArgs& p, const RowGroups& g, int64_t grid, hipStream_t stream) {
+  switch (p.fmt) {
+    case 0: return launch_groups_f<G, 0, ROWA, LAYOUT>(p, g, grid, stream);
+    case 1: return launch_groups_f<G, 1, ROWA, LAYOUT>(p, g, grid, stream);
+    case 2: return launch_groups_f<G, 2, ROWA, LAYOUT>(p, g, grid, stream);
+    case 3: return launch_groups_f<G, 3, ROWA, LAYOUT>(p, g, grid, stream);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 template <int G, int FMT, int EPI, int LAYOUT>

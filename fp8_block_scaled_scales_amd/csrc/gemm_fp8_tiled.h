@@ -9,6 +9,7 @@
 
 #include "gemm_common.h"
 #include "gemm_fp8_nt.h"
+#include "gemm_groups.h"
 
 namespace dg {
 
@@ -59,14 +60,15 @@ __device__ __forceinline__ void wait_steps(int steps) {
 // G is the K segment contracted before each promotion; the scale blocks are
 // sg x sg with sg = G << sshift (g = 256 runs G = 128 with one factor per two
 // segments). ROWA: A's factors are per row, sa is [M][K/sg]. LAYOUT bit 1: A
-// stored [K,M]; bit 0: B stored [K,N] (M resp. N any length).
+// stored [K,M]; bit 0: B stored [K,N] (M resp. N any length). GRP: as
+// gemm_fp8_nt_big's.
 template <int BM, int BN, int WM, int WN, int STAGES, int G, int GROUP_M, bool SPLIT, int FMT, int EPI, bool ROWA,
-          int LAYOUT>
+          int LAYOUT, class GRP>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
     const uint8_t* __restrict__ a, const uint8_t* __restrict__ b, const float* __restrict__ sa,
     const float* __restrict__ sb, uint16_t* __restrict__ out, int M, int N, int K, int tiles_m,
     int tiles_n, int vec_store, int ksplit, float* __restrict__ ws, int sshift, const float* __restrict__ bias,
-    int relu, const EpiArgs epi) {
+    int relu, EpiArgs epi, const GRP groups) {
   constexpr int NWAVES = WM * WN;
   constexpr int NT = 64 * NWAVES;
   constexpr int WTM = BM / WM, WTN = BN / WN;  // wave tile
@@ -91,7 +93,19 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
   const int wm = wave / WN, wn = wave % WN;
 
   int ks, tmi, tni;
-  map_tile<GROUP_M>(tiles_m, tiles_n, ks, tmi, tni);
+  if constexpr (GRP::kKind == 0) {
+    map_tile<GROUP_M>(tiles_m, tiles_n, ks, tmi, tni);
+  } else {
+    GroupTile t;
+    bool live;
+    if constexpr (GRP::kKind == 1) live = find_tile<BM, GROUP_M>(groups, tiles_n, t);
+    else live = find_tile<GROUP_M>(groups, tiles_m, tiles_n, t);
+    if (!live) return;
+    ks = 0;
+    tmi = t.tm;
+    tni = t.tn;
+    enter_group<GRP>(t, G << sshift, ROWA, a, b, sa, sb, out, epi, M, N, K);
+  }
   const int m0 = tmi * BM, n0 = tni * BN;
   const uint32_t uK = (uint32_t)K;
   const v4i ra = rsrc_words(a + (int64_t)m0 * K, (uint32_t)min(BM, M - m0) * uK);
@@ -131,12 +145,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
       stage_slab<BN, NWAVES, 2>(rb, slot + A_BYTES, uK, st * BK, wave, lane);
     }
   };
+  // with DepthGroups a block's factors of successive segments lie a row of factors apart
+  constexpr bool DEPTH = GRP::kKind == 2;
+  const int64_t sap = DEPTH ? (M - 1) / sg + 1 : 1, sbp = DEPTH ? (N - 1) / sg + 1 : 1, sar = DEPTH ? 1 : nks;
   const float* sa_row[TM];
   const float* sb_row[TN];
 #pragma unroll
-  for (int t = 0; t < TM; ++t) sa_row[t] = sa + (int64_t)min((m0 + wm * WTM + t * 32) / sg, (M - 1) / sg) * nks;
+  for (int t = 0; t < TM; ++t) sa_row[t] = sa + (int64_t)min((m0 + wm * WTM + t * 32) / sg, (M - 1) / sg) * sar;
 #pragma unroll
-  for (int t = 0; t < TN; ++t) sb_row[t] = sb + (int64_t)min((n0 + wn * WTN + t * 32) / sg, (N - 1) / sg) * nks;
+  for (int t = 0; t < TN; ++t) sb_row[t] = sb + (int64_t)min((n0 + wn * WTN + t * 32) / sg, (N - 1) / sg) * sar;
 
   v16f acc[TM][TN];
 #pragma unroll
@@ -226,10 +243,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_nt_tiled(
       }
       float sbv[TN];
 #pragma unroll
-      for (int j = 0; j < TN; ++j) sbv[j] = sb_row[j][kb >> sshift];
+      for (int j = 0; j < TN; ++j) sbv[j] = sb_row[j][(kb >> sshift) * sbp];
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const float sav = ROWA ? 0.0f : sa_row[i][kb >> sshift];
+        const float sav = ROWA ? 0.0f : sa_row[i][(kb >> sshift) * sap];
         v4f sr[4];
         if constexpr (ROWA) {
 #pragma unroll
@@ -395,10 +412,10 @@ template <int BM, int BN, int WM, int WN, int STAGES, int G, int GROUP_M, bool S
           int LAYOUT>
 static hipError_t launch_tiled_fa(const GemmArgs& p, hipStream_t stream) {
   const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((gemm_fp8_nt_tiled<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, FMT, EPI, ROWA, LAYOUT>),
+  hipLaunchKernelGGL((gemm_fp8_nt_tiled<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, FMT, EPI, ROWA, LAYOUT, NoGroups>),
                      dim3(tiles_m * tiles_n * p.ksplit), dim3(64 * WM * WN), 0, stream, p.a, p.b, p.sa, p.sb, p.out,
                      (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n, p.vec_store, p.ksplit, p.ws, p.sshift, p.bias,
-                     p.act == 1 ? 1 : 0, p.epi);
+                     p.act == 1 ? 1 : 0, p.epi, NoGroups{});
   hipError_t err = hipGetLastError();
   if constexpr (SPLIT) {
     if (p.ksplit > 1 && err == hipSuccess) {
@@ -492,6 +509,28 @@ static hipError_t launch_tiled_res(const GemmArgs& p, hipStream_t stream) {
     case 1: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 1, 0, true>(p, stream);
     case 2: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 2, 0, true>(p, stream);
     case 3: return launch_tiled_l<BM, BN, WM, WN, STAGES, G, GROUP_M, SPLIT, 3, 0, true>(p, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// The products of groups on the same tile (see big::launch_groups).
+template <int BM, int BN, int WM, int WN, int STAGES, int G, int FMT, bool ROWA, int LAYOUT, class GRP>
+static hipError_t launch_tiled_groups_f(const GemmArgs& p, const GRP& g, int64_t grid, hipStream_t stream) {
+  const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
+  constexpr int EPI = GRP::kKind == 1 ? 3 : 0;
+  hipLaunchKernelGGL((gemm_fp8_nt_tiled<BM, BN, WM, WN, STAGES, G, 4, false, FMT, EPI, ROWA, LAYOUT, GRP>), dim3((unsigned)grid),
+                     dim3(64 * WM * WN), 0, stream, p.a, p.b, p.sa, p.sb, p.out, (int)p.M, (int)p.N, (int)p.K, tiles_m, tiles_n,
+                     p.vec_store, 1, nullptr, p.sshift, nullptr, 0, p.epi, g);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, int G, bool ROWA, int LAYOUT, class GRP>
+static hipError_t launch_tiled_groups(const GemmArgs& p, const GRP& g, int64_t grid, hipStream_t stream) {
+  switch (p.fmt) {
+    case 0: return launch_tiled_groups_f<BM, BN, WM, WN, STAGES, G, 0, ROWA, LAYOUT>(p, g, grid, stream);
+    case 1: return launch_tiled_groups_f<BM, BN, WM, WN, STAGES, G, 1, ROWA, LAYOUT>(p, g, grid, stream);
+    case 2: return launch_tiled_groups_f<BM, BN, WM, WN, STAGES, G, 2, ROWA, LAYOUT>(p, g, grid, stream);
+    case 3: return launch_tiled_groups_f<BM, BN, WM, WN, STAGES, G, 3, ROWA, LAYOUT>(p, g, grid, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -512,6 +512,190 @@ int dg_epilogue_backward_fp8(const void* dout, int dout_type, int64_t lddout, co
 /* Workspace bytes of that call with dbias (DG_EINVAL for sizes it would reject). */
 int64_t dg_epilogue_backward_workspace(int64_t rows, int64_t cols, int gran, int block_rows);
 
+/* ---- Layers whose weights each row chooses: experts and adapters -----------
+ *
+ * An expert layer is sort -> quantise -> grouped product -> ... -> combine, and
+ * its way back uses the same calls (rows and combine are each other's
+ * gradients). The sort's three arrays stay on the GPU: no call needs a group's
+ * length on the host, so all of them can be captured in a graph and replayed on
+ * other routings of the same sizes. Conventions as in the section above, with
+ * these in common:
+ *
+ *   tokens, k, groups  each token has k slots (slot t*k + j), each with the index
+ *          of the group it goes to; groups <= DG_MAX_GROUPS, k <= tokens * k <=
+ *          DG_MAX_DIM. The same group may stand twice in a token.
+ *   offsets   int32 [groups + 1]: group e has the sorted rows offsets[e] ..
+ *          offsets[e+1] - 1. What a call takes is cut to 0 .. rows, so no row
+ *          outside is read or written whatever the values.
+ *   position  int32 [tokens][k]: the sorted row of each slot; a slot whose value
+ *          is not in 0 .. rows - 1 has none (its expert is elsewhere).
+ *   slot      int32 [rows]: the slot of each sorted row; -1: none, a row between
+ *          a group's last and the next group; -2: none, behind the last group.
+ *   rows      sorted rows allocated, <= DG_MAX_DIM. Rows behind the last group
+ *          are never read and are left as they were.
+ */
+
+/* Groups a call takes at most. */
+#define DG_MAX_GROUPS 1024
+
+/*
+ * dg_route_sort - the stable sort of the slots by group.
+ *
+ *   ids       [tokens][k] indices of id_bytes (4: int32, 8: int64) each, aligned
+ *             to it; a value outside 0 .. groups - 1 takes the slot out.
+ *   align     every group starts at a multiple of it (1: no rows between groups;
+ *             gran for the calls that take gran x gran factors), >= 1.
+ *   offsets, position, slot  out, 4-byte aligned, all of them fully written.
+ *   rows      at least dg_route_rows(tokens, k, groups, align).
+ *   workspace at least dg_route_sort_workspace bytes, 16-byte aligned (NULL where
+ *             that is 0); scratch, as dg_gemm_fp8_ws's.
+ */
+int dg_route_sort(const void* ids, int id_bytes, int64_t tokens, int k, int groups, int align, int32_t* offsets,
+                  int32_t* position, int32_t* slot, int64_t rows, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Rows that hold any routing of these sizes: tokens * k and align - 1 more for
+ * each group that can have a slot, cut to a multiple of align (DG_EINVAL for
+ * sizes dg_route_sort would reject). */
+int64_t dg_route_rows(int64_t tokens, int k, int groups, int align);
+
+/* Workspace bytes of dg_route_sort (DG_EINVAL for sizes it would reject). */
+int64_t dg_route_sort_workspace(int64_t tokens, int k, int groups);
+
+/*
+ * dg_route_quantize_fp8 - tokens as FP8 rows in sorted order:
+ *
+ *   v[r] = weights[slot[r]] * x[slot[r] / k]  in FP32 (no weights: x itself)
+ *   scales, q: the quantisers' rule on v, in gran x gran blocks of sorted rows
+ *              (block_rows = gran) or one factor per row and segment (1)
+ *
+ * The dispatch to the experts and, with the combine's weights on its output's
+ * gradient, the combine's gradient. Rows between groups get codes of zero (and
+ * with block_rows = 1 factors of 1); rows behind the last group, and factors of
+ * blocks that begin there, are left as they were. A slot has to be told the same
+ * way by position and slot, as dg_route_sort does.
+ *
+ *   x        [tokens][cols] of x_type, row pitch ldx; 16-byte aligned base and
+ *            pitch.  weights  FP32 [tokens][k] or NULL.
+ *   gran     64, 128 or 256, dividing cols.  fmt  DG_FMT_E4M3 or DG_FMT_E5M2.
+ *   q        FP8 codes out, [rows][cols], 16-byte aligned.
+ *   scales   FP32 out, [ceil(rows/block_rows)][cols/gran]; with gran x gran
+ *            blocks at most 2^22 - 1 of them.
+ *   workspace at least dg_route_quantize_workspace bytes, 16-byte aligned (NULL
+ *            where that is 0); scratch, as dg_gemm_fp8_ws's.
+ */
+int dg_route_quantize_fp8(const void* x, int x_type, int64_t ldx, int64_t tokens, int64_t cols, int k,
+                          const int32_t* position, const int32_t* slot, int64_t rows, const float* weights, int gran,
+                          int block_rows, int fmt, void* q, float* scales, void* workspace, int64_t workspace_bytes,
+                          void* stream);
+
+/* Workspace bytes of that call (DG_EINVAL for sizes it would reject). */
+int64_t dg_route_quantize_workspace(int64_t tokens, int64_t cols, int k, int64_t rows, int gran, int block_rows);
+
+/*
+ * dg_route_combine - every token's rows brought back:
+ *
+ *   out[t] = res[t] + sum over j of weights[t][j] * y[position[t][j]]
+ *
+ * summed in FP32 in the order of j, the residual last, rounded once. Slots
+ * without a row add nothing. Without weights (1 each) and res it is the gradient
+ * of the dispatch.
+ *
+ *   y        [rows][cols] of y_type, row pitch ldy.
+ *   weights  FP32 [tokens][k] or NULL.
+ *   res      [tokens][cols] of out_type, row pitch ldres, or NULL; may be out
+ *            itself (ldres = cols).
+ *   out      out, [tokens][cols] of out_type.
+ *   cols     a multiple of 8. y, res, out: 16-byte aligned bases and pitches.
+ */
+int dg_route_combine(const void* y, int y_type, int64_t ldy, int64_t rows, int64_t tokens, int64_t cols, int k,
+                     const int32_t* position, const float* weights, const void* res, int64_t ldres, void* out, int out_type,
+                     void* stream);
+
+/*
+ * dg_route_weight_grad - the gradient of the combine's weights:
+ *
+ *   dweights[t][j] = sum over c of dout[t][c] * y[position[t][j]][c]
+ *
+ * in FP32, 0 for slots without a row. dout [tokens][cols] of dout_type (row pitch
+ * lddout), y [rows][cols] of y_type (ldy), cols a multiple of 8; 16-byte aligned
+ * bases and pitches. dweights FP32 [tokens][k] out.
+ */
+int dg_route_weight_grad(const void* dout, int dout_type, int64_t lddout, const void* y, int y_type, int64_t ldy,
+                         int64_t rows, int64_t tokens, int64_t cols, int k, const int32_t* position, float* dweights,
+                         void* stream);
+
+/*
+ * dg_gemm_fp8_grouped - the products of the groups' rows with their own B:
+ *
+ *   z = C[r,j] of dg_gemm_fp8_layout with A row r and B_e, e the group of row r
+ *   pre[r,j] = bf16(z);  out[r,j] = bf16(act(z))
+ *
+ *   a, sa    A codes [rows][K] and factors: [rows][K/gran] with sa_rows = 1, or
+ *            [ceil(rows/gran)][K/gran] with sa_rows = gran, and then every group
+ *            has to start at a multiple of gran.
+ *   b        [groups] matrices one after the other, each [N][K] (layout
+ *            DG_LAYOUT_NT) or [K][N] (DG_LAYOUT_NN: the gradient of the rows).
+ *   sb       [groups][ceil(N/gran)][K/gran], the logical factors, whatever the layout.
+ *   out      BF16 [rows][N]; pre BF16 [rows][N] or NULL: rows of the groups are
+ *            written (those between a group's slots and the next group too, of
+ *            codes of zero), rows behind the last group are left as they were.
+ *   act      any of the five DG_ACT_* codes.
+ *
+ * M, N, K, gran, formats, alignments and status codes as dg_gemm_fp8_layout, with
+ * M = rows. A row's result does not depend on the other rows' values, but its sums'
+ * order may change with rows, groups, N and K, which choose the tile.
+ */
+int dg_gemm_fp8_grouped(const void* a, const void* b, const float* sa, const float* sb, const int32_t* offsets,
+                        int groups, void* out, int64_t rows, int64_t N, int64_t K, int gran, int layout, int sa_rows,
+                        int fmt_a, int fmt_b, int act, void* pre, void* stream);
+
+/*
+ * dg_gemm_fp8_grouped_wgrad - the gradient of the groups' weights:
+ *
+ *   out[e][i][j] = bf16( sum over the rows r of group e of A[r,i] * B[r,j] )
+ *
+ * on FP8 codes with gran x gran blocks along the rows, as dg_gemm_fp8_layout's TN.
+ * A group without rows gives zeros. Every group has to start at a multiple of gran,
+ * and the rows between groups hold codes of zero (or any finite gradient: they count).
+ *
+ *   a, sa    A codes [rows][M] and their factors [rows/gran][M/gran], as the
+ *            quantisers leave them.  b, sb: [rows][N], [rows/gran][N/gran].
+ *   out      BF16 [groups][M][N].
+ *   rows, M, N  multiples of gran, <= DG_MAX_DIM.
+ */
+int dg_gemm_fp8_grouped_wgrad(const void* a, const void* b, const float* sa, const float* sb, const int32_t* offsets,
+                              int groups, void* out, int64_t rows, int64_t M, int64_t N, int gran, int fmt_a, int fmt_b,
+                              void* stream);
+
+/*
+ * dg_lora - low-rank adapters, one per row, beside a shared projection:
+ *
+ *   out[t] = base[t] + scale[l] * (x[t] A_l^T) B_l^T,  l the group of row t
+ *
+ * for rows sorted by adapter with dg_route_sort (k = 1, align = 1, rows =
+ * tokens; once for all projections of a step). A row without an adapter is base
+ * alone. Sums in FP32; x A^T enters the second product with at least 16 bits; one
+ * rounding at the end.
+ *
+ *   x        [tokens][K] of type DG_IN_BF16 or DG_IN_F16, row pitch ldx.
+ *   a, b     [groups][rank][K] and [groups][N][rank] of x's type.
+ *   scale    FP32 [groups], or NULL (1 each).
+ *   base     [tokens][N] of out_type, row pitch ldbase, aligned to its element, or
+ *            NULL (zero); may be out itself (ldbase = N): updated in place.
+ *   out      out, [tokens][N] of out_type (any of the three), aligned to its element.
+ *   K, rank  multiples of 8, rank <= 128; N any. x, a, b: 16-byte aligned bases and
+ *            pitches.
+ *   workspace at least dg_lora_workspace bytes, 16-byte aligned; scratch, as
+ *            dg_gemm_fp8_ws's: calls that may overlap in time need distinct ones.
+ */
+int dg_lora(const void* x, int type, int64_t ldx, int64_t tokens, int64_t K, const void* a, const void* b,
+            const float* scale, int64_t N, int rank, int groups, const int32_t* offsets, const int32_t* position,
+            const int32_t* slot, const void* base, int64_t ldbase, void* out, int out_type, void* workspace,
+            int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of that call (DG_EINVAL for sizes it would reject). */
+int64_t dg_lora_workspace(int64_t tokens, int64_t K, int64_t N, int rank, int groups);
+
 /* Text for a status code (for DG_ELAUNCH: the last HIP error on this
  * thread), so a caller can log which class of failure (the pitfalls article
  * §5.4: recoverable or not) it met. The string is static, or thread-local for
