@@ -64,39 +64,47 @@ __global__ __launch_bounds__(kThreads) void lora_shrink(const LoraArgs p, const 
   GroupTile t;
   if (!find_tile<BM, 1>(grp, p.splits, t)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
-  const int steps = (int)((p.K + 31) / 32);
+  const int steps = (int)((p.K + 63) / 64), whole = (int)(p.K / 64);
   const int s0 = (int)((int64_t)t.tn * steps / p.splits), s1 = (int)((int64_t)(t.tn + 1) * steps / p.splits);
   const int w0 = s0 + (int)((int64_t)wave * (s1 - s0) / kWaves), w1 = s0 + (int)((int64_t)(wave + 1) * (s1 - s0) / kWaves);
-  const uint16_t* const a = static_cast<const uint16_t*>(p.a) + (int64_t)t.group * p.rank * p.K;
-  const uint16_t* xr[MT];
-  bool has[MT];
+  // Rows past the group's, or without a token, and ranks past the last read a row
+  // that there is: their sums are their own and are not kept.
+  const uint16_t* const a = static_cast<const uint16_t*>(p.a) + (int64_t)t.group * p.rank * p.K + 16 * q;
+  const uint16_t *xr[MT], *ar[NR];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int r = t.tm * BM + m * 16 + i16;
-    const int tok = r < t.rows ? token_of(p, t.row0 + r) : -1;
-    has[m] = tok >= 0;
-    xr[m] = static_cast<const uint16_t*>(p.x) + (int64_t)max(tok, 0) * p.ldx + 8 * q;
+    xr[m] = static_cast<const uint16_t*>(p.x) + (int64_t)max(r < t.rows ? token_of(p, t.row0 + r) : 0, 0) * p.ldx + 16 * q;
   }
+#pragma unroll
+  for (int n = 0; n < NR; ++n) ar[n] = a + (int64_t)min(n * 16 + i16, p.rank - 1) * p.K;
   v4f acc[MT][NR];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NR; ++n) acc[m][n] = (v4f){};
-#pragma unroll 4
-  for (int s = w0; s < w1; ++s) {
-    const int64_t k = (int64_t)s * 32;
-    const bool in = k + 8 * q < p.K;
-    v4u xa[MT], ra[NR];
+  // 64 of K a step: a lane's two pieces of 8 elements are neighbours, so that the
+  // four lanes of a row ask for its whole 128-byte line at once
+  auto step = [&](int s, auto in) {
+    const int64_t k = (int64_t)s * 64;
+    v4u xa[2][MT], ra[2][NR];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xa[m] = in && has[m] ? *reinterpret_cast<const v4u*>(xr[m] + k) : (v4u){};
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
-      ra[n] = in && n * 16 + i16 < p.rank ? *reinterpret_cast<const v4u*>(a + (int64_t)(n * 16 + i16) * p.K + k + 8 * q) : (v4u){};
+      for (int m = 0; m < MT; ++m) xa[h][m] = in(h) ? *reinterpret_cast<const v4u*>(xr[m] + k + 8 * h) : (v4u){};
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NR; ++n) ra[h][n] = in(h) ? *reinterpret_cast<const v4u*>(ar[n] + k + 8 * h) : (v4u){};
+    }
 #pragma unroll
-      for (int n = 0; n < NR; ++n) acc[m][n] = mfma16x32<XK>(xa[m], ra[n], acc[m][n]);
-  }
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NR; ++n) acc[m][n] = mfma16x32<XK>(xa[h][m], ra[h][n], acc[m][n]);
+  };
+#pragma unroll 2
+  for (int s = w0; s < min(w1, whole); ++s) step(s, [](int) { return true; });
+  if (w0 <= whole && whole < w1) step(whole, [&](int h) { return (int64_t)whole * 64 + 16 * q + 8 * h < p.K; });
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -120,40 +128,56 @@ constexpr int kStrip = 64;  // columns of a wave's step
 typedef v4u v4u_at2 __attribute__((aligned(2)));
 typedef v4f v4f_at4 __attribute__((aligned(4)));
 
-// 16 consecutive outputs of a token from column n on.
+// 16 bytes of consecutive outputs of a token, from column n on: the base's as
+// they are stored (16-bit elements one to a word where the row ends inside).
 template <int OK>
-__device__ __forceinline__ void add_store(const LoraArgs& p, int64_t tok, int64_t n, const float (&d)[16]) {
-  constexpr int PER = 16 / InKind<OK>::kBytes;  // elements of 16 bytes
+struct Out16 {
+  static constexpr int B = InKind<OK>::kBytes, PER = 16 / B;
   typedef typename std::conditional<OK == 0, v4f_at4, v4u_at2>::type V;
-  char* const out = static_cast<char*>(p.out) + (tok * p.N + n) * InKind<OK>::kBytes;
-  const char* const base = static_cast<const char*>(p.base) + (tok * p.ldbase + n) * InKind<OK>::kBytes;
-  if (n + 16 <= p.N) {
+};
+
+template <int OK>
+__device__ __forceinline__ void load_base(const LoraArgs& p, int64_t tok, int64_t n, unsigned (&w)[Out16<OK>::PER]) {
+  typedef Out16<OK> O;
 #pragma unroll
-    for (int i = 0; i < 16 / PER; ++i) {
-      float f[PER];
+  for (int e = 0; e < O::PER; ++e) w[e] = 0;
+  if (!p.base || n >= p.N) return;
+  const char* const base = static_cast<const char*>(p.base) + (tok * p.ldbase + n) * O::B;
+  if (n + O::PER <= p.N) {
+    const v4u v = __builtin_bit_cast(v4u, *reinterpret_cast<const typename O::V*>(base));
 #pragma unroll
-      for (int e = 0; e < PER; ++e) f[e] = 0.0f;
-      if (p.base) {
-        const v4u w = __builtin_bit_cast(v4u, *reinterpret_cast<const V*>(base + 16 * i));
-        Raw<OK, PER> raw;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) raw.w[e] = w[e];
-        widen_raw(raw, f);
-      }
-#pragma unroll
-      for (int e = 0; e < PER; ++e) f[e] += d[i * PER + e];
-      const Raw<OK, PER> r = round_raw<OK>(f);
-      *reinterpret_cast<V*>(out + 16 * i) = __builtin_bit_cast(V, (v4u){r.w[0], r.w[1], r.w[2], r.w[3]});
-    }
+    for (int e = 0; e < 4; ++e) w[e] = v[e];
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < O::PER; ++e) {
+      if (n + e >= p.N) break;
+      w[e] = OK == 0 ? reinterpret_cast<const uint32_t*>(base)[e] : reinterpret_cast<const uint16_t*>(base)[e];
+    }
+  }
+}
+
+template <int OK>
+__device__ __forceinline__ void add_store(const LoraArgs& p, int64_t tok, int64_t n, const float (&d)[Out16<OK>::PER],
+                                          const unsigned (&w)[Out16<OK>::PER]) {
+  typedef Out16<OK> O;
+  if (n >= p.N) return;
+  char* const out = static_cast<char*>(p.out) + (tok * p.N + n) * O::B;
+  if (n + O::PER <= p.N) {
+    float f[O::PER];
+    widen_raw(Raw<OK, O::PER>{{w[0], w[1], w[2], w[3]}}, f);
+#pragma unroll
+    for (int e = 0; e < O::PER; ++e) f[e] += d[e];
+    const Raw<OK, O::PER> r = round_raw<OK>(f);
+    *reinterpret_cast<typename O::V*>(out) = __builtin_bit_cast(typename O::V, (v4u){r.w[0], r.w[1], r.w[2], r.w[3]});
+  } else {
+#pragma unroll
+    for (int e = 0; e < O::PER; ++e) {
       if (n + e >= p.N) break;
       if constexpr (OK == 0) {
-        reinterpret_cast<float*>(out)[e] = (p.base ? reinterpret_cast<const float*>(base)[e] : 0.0f) + d[e];
+        reinterpret_cast<float*>(out)[e] = __uint_as_float(w[e]) + d[e];
       } else {
-        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (p.base) widen_raw(Raw<OK, 4>{{reinterpret_cast<const uint16_t*>(base)[e], 0u}}, f);
+        float f[4];
+        widen_raw(Raw<OK, 4>{{w[e], 0u}}, f);
         f[0] += d[e];
         reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)round_raw<OK>(f).w[0];
       }
@@ -197,10 +221,18 @@ __device__ __forceinline__ void split16(float f, uint16_t (&t)[TERMS]) {
   }
 }
 
+// The column of row i of the strip's product s (0 .. 3): 32-bit outputs as they
+// come, 16-bit ones in pairs of products that share 32 columns.
+template <int OK>
+__device__ __forceinline__ int strip_col(int s, int i) {
+  return OK == 0 ? 16 * s + i : 32 * (s >> 1) + 8 * (i >> 2) + 4 * (s & 1) + (i & 3);
+}
+
 // out of MT x 16 rows by `strips` x 4 x 64 columns. The rows of B_l are the
-// first operand, so that a lane ends with outputs of one token; of a 64-column
-// strip the four products take columns 16 (i / 4) + 4 s + i % 4 (s = 0 .. 3),
-// which gives a lane 16 consecutive ones. KS: 32-wide steps of the rank.
+// first operand, so that a lane ends with outputs of one token. Which columns of a
+// 64-column strip a product's 16 rows stand for is free (strip_col): those that
+// give a lane 16 bytes of consecutive outputs, and four neighbouring lanes 64.
+// KS: 32-wide steps of the rank.
 template <int XK, int OK, int MT, int KS>
 __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const RowGroups grp, unsigned tile_wgs, int strips) {
   constexpr int BM = 16 * MT, RP = 32 * KS, LD = RP + 8;  // pitch in 16-bit elements: 16-byte reads of 16 rows on distinct banks
@@ -273,15 +305,25 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
   for (int st = 0; st < strips; ++st) {
     const int64_t n0 = (((int64_t)t.tn * strips + st) * kWaves + wave) * kStrip;
     if (n0 >= p.N) return;
+    // a strip's outputs: 64 bytes of 16-bit ones in two pieces per lane, of FP32 in four
+    constexpr int PER = Out16<OK>::PER, PIECES = 16 / PER;
     v4u br[KS][4];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const int64_t n = n0 + 16 * (i16 >> 2) + 4 * s + (i16 & 3);
-        const int k = 32 * ks + 8 * q;
-        br[ks][s] = n < p.N && k < p.rank ? *reinterpret_cast<const v4u*>(b + n * p.rank + k) : (v4u){};
+        // past the last column a column that there is (not stored), past the rank
+        // elements that there are (v is zero there)
+        const int64_t n = min(n0 + strip_col<OK>(s, i16), p.N - 1);
+        br[ks][s] = *reinterpret_cast<const v4u*>(b + n * p.rank + min(32 * ks + 8 * q, p.rank - 8));
       }
+    // all of the base ahead of the first store, which may be to the same memory
+    unsigned old[MT][PIECES][PER];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < PIECES; ++h)
+        if (tok[m] >= 0) load_base<OK>(p, tok[m], n0 + strip_col<OK>(h * (4 / PIECES), 4 * q), old[m][h]);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       v4f acc[4];
@@ -295,13 +337,14 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
 #pragma unroll
           for (int s = 0; s < 4; ++s) acc[s] = mfma16x32<XK>(br[ks][s], h, acc[s]);
         }
-      if (tok[m] < 0 || n0 + 16 * q >= p.N) continue;
-      float d[16];
+      if (tok[m] < 0) continue;
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int h = 0; h < PIECES; ++h) {
+        float d[PER];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) d[4 * s + v] = acc[s][v] * up[m];
-      add_store<OK>(p, tok[m], n0 + 16 * q, d);
+        for (int e = 0; e < PER; ++e) d[e] = acc[h * (4 / PIECES) + e / 4][e % 4] * up[m];
+        add_store<OK>(p, tok[m], n0 + strip_col<OK>(h * (4 / PIECES), 4 * q), d, old[m][h]);
+      }
     }
   }
 }

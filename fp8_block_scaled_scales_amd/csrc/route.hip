@@ -31,7 +31,7 @@ constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
 // Slots that one workgroup sorts alone; beyond, chunks of at least kChunk slots,
 // at most 256 of them, are counted by one launch and placed by a second.
-constexpr int64_t kOneSort = 8192, kChunk = 4096;
+constexpr int64_t kOneSort = 4096, kChunk = 1024;
 
 int64_t sort_chunk(int64_t n) { return std::max<int64_t>(kChunk, ((n + 255) / 256 + 1023) / 1024 * 1024); }
 
@@ -183,32 +183,56 @@ hipError_t launch_sort_t(const SortArgs& p, hipStream_t stream) {
 
 // ---- rows as FP8 codes --------------------------------------------------------
 
+// quant_common.h's div_by_scale in five instructions: the remainder is taken
+// with its sign turned (q s - x), which leaves a zero the sign of x by itself (q =
+// -0 gives a remainder of +0, and -(+0) inv + -0 is -0), so no sign is copied.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  float q = x * inv;
+  q = __builtin_fmaf(-__builtin_fmaf(q, s, -x), inv, q);
+  return __builtin_fmaf(-__builtin_fmaf(q, s, -x), inv, q);
+}
+
+// A wave whose factors all have normal reciprocals divides by them; where one has
+// not, every lane of it takes the quantisers' two ways (the same codes).
 template <int FMT, int E>
-__device__ __forceinline__ void codes_fmt(const float (&y)[E], float s, int (&c)[E / 4]) {
+__device__ __forceinline__ void codes_fmt(const float (&y)[E], float s, float inv, int (&c)[E / 4]) {
   const bool fast = recip_ok(s);
-  const float inv = 1.0f / s;
+  if (__all(fast)) {
 #pragma unroll
-  for (int i = 0; i < E / 4; ++i) {
-    const v4f v = {y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
-    if (fast) c[i] = encode4<FMT, true>(v, s, inv);
-    else c[i] = encode4<FMT, false>(v, s, inv);
+    for (int i = 0; i < E / 4; ++i) {
+      const int lo = cvt2<FMT, false>(quotient(y[4 * i], s, inv), quotient(y[4 * i + 1], s, inv), 0);
+      c[i] = cvt2<FMT, true>(quotient(y[4 * i + 2], s, inv), quotient(y[4 * i + 3], s, inv), lo);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      const v4f v = {y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
+      if (fast) c[i] = encode4<FMT, true>(v, s, inv);
+      else c[i] = encode4<FMT, false>(v, s, inv);
+    }
   }
 }
 
+// The codes of y / s, inv = 1 / s.
 template <int E>
-__device__ __forceinline__ void codes_of(const float (&y)[E], float s, int fmt, int (&c)[E / 4]) {
-  if (fmt == 1) codes_fmt<1>(y, s, c);
-  else codes_fmt<0>(y, s, c);
+__device__ __forceinline__ void codes_of(const float (&y)[E], float s, float inv, int fmt, int (&c)[E / 4]) {
+  if (fmt == 1) codes_fmt<1>(y, s, inv, c);
+  else codes_fmt<0>(y, s, inv, c);
 }
 
-template <int E>
+template <bool ONCE, int E>
 __device__ __forceinline__ void put_codes(uint8_t* q, const int (&c)[E / 4]) {
-  if constexpr (E == 8) *reinterpret_cast<v2i*>(q) = (v2i){c[0], c[1]};
-  else *reinterpret_cast<int*>(q) = c[0];
+  if constexpr (E == 8) {
+    if constexpr (ONCE) __builtin_nontemporal_store((v2i){c[0], c[1]}, reinterpret_cast<v2i*>(q));
+    else *reinterpret_cast<v2i*>(q) = (v2i){c[0], c[1]};
+  } else {
+    if constexpr (ONCE) __builtin_nontemporal_store(c[0], reinterpret_cast<int*>(q));
+    else *reinterpret_cast<int*>(q) = c[0];
+  }
 }
 
-// Rows between a group's last and the next group: codes of zero, factors of
-// one. A wave looks at 64 rows.
+// Rows between a group's last and the next group: codes of zero and, with a
+// factor per row, factors of one. A wave looks at 64 rows.
 __device__ __forceinline__ void pad_rows(const RouteQuantArgs& p, int64_t wave, int lane) {
   const int64_t r0 = wave * 64;
   const int s = r0 + lane < p.rows ? p.slot[r0 + lane] : -2;
@@ -218,49 +242,172 @@ __device__ __forceinline__ void pad_rows(const RouteQuantArgs& p, int64_t wave, 
     const int64_t r = r0 + __builtin_ctzll(m);
     m &= m - 1;
     for (int64_t c = lane * 16; c < p.cols; c += 64 * 16) *reinterpret_cast<v4u*>(p.q + r * p.cols + c) = (v4u){};
-    for (int64_t c = lane; c < segs; c += 64) p.scales[r * segs + c] = 1.0f;
+    if (p.block_rows == 1)
+      for (int64_t c = lane; c < segs; c += 64) p.scales[r * segs + c] = 1.0f;
   }
 }
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kRowWaves = kRowThreads / 64;
 
-// 1 x g: a lane takes E columns of a token and writes their codes to every row
-// that the token has.
-template <int XK, bool W>
-__global__ __launch_bounds__(kRowThreads) void route_rows(const RouteQuantArgs p, int64_t units, unsigned unit_wgs) {
+// How a wave of the token kernels takes its share: U units of E columns per
+// lane, 64 E apart, from column `c0` of token `t` on.
+template <int E, int U>
+struct Piece {
+  int64_t c0;
+  __device__ __forceinline__ int64_t col(int u, int lane) const { return c0 + (int64_t)(u * 64 + lane) * E; }
+};
+
+// The tokens' rows, codes of every one of them: a wave takes a piece of a token,
+// whose k rows and weights its lanes load at once, in flight with the token's
+// columns. OWN: 1 x g, the factors are the token's own segments' (with weights:
+// each row's, since |w x| is largest where |x| is: rounding keeps order);
+// otherwise the factors of g x g blocks are in scales already.
+template <int XK, bool W, bool OWN, int U, bool ONCE>
+__global__ __launch_bounds__(kRowThreads) void route_rows(const RouteQuantArgs p, int pieces, int token_wgs) {
   constexpr int E = unit_of(XK, 1);
-  if (blockIdx.x >= unit_wgs) {
-    const int64_t wave = (int64_t)(blockIdx.x - unit_wgs) * (kRowThreads / 64) + (threadIdx.x >> 6);
-    const int64_t waves = (int64_t)(gridDim.x - unit_wgs) * (kRowThreads / 64);
-    for (int64_t w = wave; w * 64 < p.rows; w += waves) pad_rows(p, w, threadIdx.x & 63);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit_wgs = pieces * token_wgs;
+  if ((int)blockIdx.x >= unit_wgs) {
+    const int64_t first = (int64_t)((int)blockIdx.x - unit_wgs) * kRowWaves + wave, step = (int64_t)((int)gridDim.x - unit_wgs) * kRowWaves;
+    for (int64_t w = first; w * 64 < p.rows; w += step) pad_rows(p, w, lane);
     return;
   }
-  const int64_t per = p.cols / E, segs = p.cols / p.gran;
-  // whole segments are live or not, so each reduction stays inside live lanes
-  for (int64_t u = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; u < units; u += (int64_t)unit_wgs * kRowThreads) {
-    const int64_t t = u / per, c = (u - t * per) * E;
-    float x[E];
-    widen_raw(load_raw<XK, E>(p.x, t * p.ldx + c), x);
-    const float top = segment_max<E>(amax_of(x), p.gran);
-    const bool leads = (c & (p.gran - 1)) == 0;
-    float s = block_scale(top, format_max(p.fmt));
-    int code[E / 4];
-    if constexpr (!W) codes_of(x, s, p.fmt, code);
-    for (int j = 0; j < p.k; ++j) {
-      const int r = p.position[t * p.k + j];
-      if (r < 0 || r >= p.rows) continue;
-      if constexpr (W) {
-        // rounding keeps order: the largest |w x| is that of the largest |x|
-        const float w = p.weights[t * p.k + j];
-        s = block_scale(fabsf(top * w), format_max(p.fmt));
-        float y[E];
+  const Piece<E, U> piece{(int64_t)((int)blockIdx.x % pieces) * (64 * E * U)};
+  const int64_t segs = p.cols / p.gran;
+  const int gshift = 31 - __builtin_clz(p.gran);
+  const float fmax = format_max(p.fmt);
+  const float* const invs = p.ws + p.tokens * segs;  // of g x g blocks
+  for (int64_t t = (int64_t)((int)blockIdx.x / pieces) * kRowWaves + wave; t < p.tokens; t += (int64_t)token_wgs * kRowWaves) {
+    int rows = lane < p.k ? p.position[t * p.k + lane] : -1;
+    float ws = W && lane < p.k ? p.weights[t * p.k + lane] : 0.0f;
+    float x[U][E], top[U], own[U];
+    int code[U][E / 4];
+    bool live[U];  // whole segments are live or not, so each reduction stays inside live lanes
 #pragma unroll
-        for (int i = 0; i < E; ++i) y[i] = x[i] * w;
-        codes_of(y, s, p.fmt, code);
-      }
-      put_codes<E>(p.q + (int64_t)r * p.cols + c, code);
-      if (leads) p.scales[(int64_t)r * segs + c / p.gran] = s;
+    for (int u = 0; u < U; ++u) {
+      live[u] = piece.col(u, lane) < p.cols;
+      if (live[u]) widen_raw(load_raw<XK, E>(p.x, t * p.ldx + piece.col(u, lane)), x[u]);
     }
+    // g x g: the factors of the next of the token's rows are on their way while one is coded
+    float s[U], inv[U], s1[U], inv1[U];
+    auto fetch = [&](int r) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = (int64_t)(r >> gshift) * segs + (piece.col(u, lane) >> gshift);
+        const bool has = live[u] && r >= 0 && r < p.rows;
+        s1[u] = has ? p.scales[at] : 1.0f;
+        inv1[u] = has ? invs[at] : 1.0f;
+      }
+    };
+    if constexpr (!OWN) fetch(__builtin_amdgcn_readlane(rows, 0));
+    if constexpr (OWN) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!live[u]) continue;
+        top[u] = segment_max<E>(amax_of(x[u]), p.gran);
+        if constexpr (!W) {
+          own[u] = block_scale(top[u], fmax);
+          codes_of(x[u], own[u], 1.0f / own[u], p.fmt, code[u]);
+        }
+      }
+    }
+    for (int j = 0; j < p.k; ++j) {
+      const int r = __builtin_amdgcn_readlane(rows, j & 63);
+      const float w = W ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws), j & 63)) : 1.0f;
+      if (j + 1 < p.k && ((j + 1) & 63) == 0) {  // more than 64 choices
+        rows = j + 1 + lane < p.k ? p.position[t * p.k + j + 1 + lane] : -1;
+        if constexpr (W) ws = j + 1 + lane < p.k ? p.weights[t * p.k + j + 1 + lane] : 0.0f;
+      }
+      if constexpr (!OWN) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          s[u] = s1[u];
+          inv[u] = inv1[u];
+        }
+        if (j + 1 < p.k) fetch(__builtin_amdgcn_readlane(rows, (j + 1) & 63));
+      }
+      if (r < 0 || r >= p.rows) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!live[u]) continue;
+        const int64_t c = piece.col(u, lane);
+        if constexpr (W || !OWN) {
+          float y[E];
+#pragma unroll
+          for (int i = 0; i < E; ++i) y[i] = W ? x[u][i] * w : x[u][i];
+          if constexpr (OWN) {
+            s[u] = block_scale(fabsf(top[u] * w), fmax);
+            inv[u] = 1.0f / s[u];
+          }
+          codes_of(y, s[u], inv[u], p.fmt, code[u]);
+        } else {
+          s[u] = own[u];
+        }
+        put_codes<ONCE, E>(p.q + (int64_t)r * p.cols + c, code[u]);
+        if (OWN && (c & (p.gran - 1)) == 0) p.scales[(int64_t)r * segs + (c >> gshift)] = s[u];
+      }
+    }
+  }
+}
+
+// Every token's segment maxima, for the factors of g x g blocks.
+template <int XK, int U>
+__global__ __launch_bounds__(kRowThreads) void route_maxima(const RouteQuantArgs p, int pieces, int token_wgs) {
+  constexpr int E = unit_of(XK, 1);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Piece<E, U> piece{(int64_t)((int)blockIdx.x % pieces) * (64 * E * U)};
+  const int64_t segs = p.cols / p.gran;
+  for (int64_t t = (int64_t)((int)blockIdx.x / pieces) * kRowWaves + wave; t < p.tokens; t += (int64_t)token_wgs * kRowWaves) {
+    Raw<XK, E> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (piece.col(u, lane) < p.cols) raw[u] = load_raw<XK, E>(p.x, t * p.ldx + piece.col(u, lane));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = piece.col(u, lane);
+      if (c >= p.cols) continue;
+      float x[E];
+      widen_raw(raw[u], x);
+      const float top = segment_max<E>(amax_of(x), p.gran);
+      if ((c & (p.gran - 1)) == 0) p.ws[t * segs + c / p.gran] = top;
+    }
+  }
+}
+
+// The factors of g x g blocks of sorted rows from the tokens' maxima, and their
+// reciprocals (behind the maxima) for the many divisions that follow: a
+// workgroup takes a row of blocks, 32 of them, its threads 32 rows at a time.
+constexpr int kFactorThreads = 1024;
+
+template <bool W>
+__global__ __launch_bounds__(kFactorThreads) void route_factors(const RouteQuantArgs p, int seg_wgs) {
+  constexpr int CL = 32, RL = kFactorThreads / CL;
+  __shared__ float red[RL][CL];
+  const int64_t segs = p.cols / p.gran;
+  const int64_t rb = (int)blockIdx.x / seg_wgs;
+  if (p.slot[rb * p.gran] == -2) return;  // behind the last group
+  const int cl = threadIdx.x % CL, rl = threadIdx.x / CL;
+  const int64_t seg = (int64_t)((int)blockIdx.x % seg_wgs) * CL + cl;
+  const int64_t slots = p.tokens * p.k, end = min(rb * p.gran + p.gran, p.rows);
+  float top = 0.0f;
+  if (seg < segs) {
+#pragma unroll 8
+    for (int64_t r = rb * p.gran + rl; r < end; r += RL) {
+      const int s = p.slot[r];
+      if (s < 0 || s >= slots) continue;
+      float v = p.ws[(int64_t)((unsigned)s / (unsigned)p.k) * segs + seg];
+      if constexpr (W) v = fabsf(v * p.weights[s]);
+      top = fmaxf(top, v);
+    }
+  }
+  red[rl][cl] = top;
+  __syncthreads();
+  if (rl == 0 && seg < segs) {
+#pragma unroll
+    for (int i = 1; i < RL; ++i) top = fmaxf(top, red[i][cl]);
+    const float s = block_scale(top, format_max(p.fmt));
+    p.scales[rb * segs + seg] = s;
+    p.ws[p.tokens * segs + rb * segs + seg] = 1.0f / s;
   }
 }
 
@@ -302,35 +449,65 @@ __global__ __launch_bounds__(NT) void route_blocks(const RouteQuantArgs p) {
   top = red[0];
 #pragma unroll
   for (int w = 1; w < NT / 64; ++w) top = fmaxf(top, red[w]);
-  const float s = block_scale(top, format_max(p.fmt));
+  const float s = block_scale(top, format_max(p.fmt)), inv = 1.0f / s;
   if (t == 0) p.scales[rb * ncb + cb] = s;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int64_t r = rb * G + i * RPP + rsub;
     if (r < p.rows && p.slot[r] != -2) {
       int code[E / 4];
-      codes_of(z[i], s, p.fmt, code);
-      put_codes<E>(p.q + r * p.cols + c, code);
+      codes_of(z[i], s, inv, p.fmt, code);
+      put_codes<false, E>(p.q + r * p.cols + c, code);
     }
   }
 }
 
 constexpr int64_t kMaxWgs = 1 << 20;
 
+// g x g blocks of this many codes or more: three launches that read every token
+// twice, instead of one that gathers every row of a block.
+constexpr int64_t kByTokens = 1ll << 23;
+
+bool by_tokens(int64_t rows, int64_t cols) { return rows * cols >= kByTokens; }
+
+// Units per lane: four where that leaves the chip enough waves.
+template <int E>
+int units_per_lane(int64_t tokens, int64_t cols) {
+  return cols >= 64 * E * 4 && tokens * (cols / (64 * E * 4)) >= 4096 ? 4 : 1;
+}
+
+template <int XK, bool W, bool OWN, int U>
+hipError_t launch_tokens(const RouteQuantArgs& p, hipStream_t stream) {
+  constexpr int E = unit_of(XK, 1);
+  const int64_t pieces = (p.cols + 64 * E * U - 1) / (64 * E * U);
+  const int64_t tokens = std::min((p.tokens + kRowWaves - 1) / kRowWaves, std::max<int64_t>(1, kMaxWgs / pieces));
+  const int64_t pads = std::min<int64_t>((p.rows + kRowThreads - 1) / kRowThreads, kMaxWgs);
+  if constexpr (!OWN) {
+    hipLaunchKernelGGL((route_maxima<XK, U>), dim3((unsigned)(pieces * tokens)), dim3(kRowThreads), 0, stream, p, (int)pieces, (int)tokens);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const int64_t segs = (p.cols / p.gran + 31) / 32;
+    hipLaunchKernelGGL((route_factors<W>), dim3((unsigned)((p.rows + p.gran - 1) / p.gran * segs)), dim3(kFactorThreads), 0, stream, p, (int)segs);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  const dim3 grid((unsigned)(pieces * tokens + pads));
+  if (p.rows * p.cols >= kOnceBytes)
+    hipLaunchKernelGGL((route_rows<XK, W, OWN, U, true>), grid, dim3(kRowThreads), 0, stream, p, (int)pieces, (int)tokens);
+  else
+    hipLaunchKernelGGL((route_rows<XK, W, OWN, U, false>), grid, dim3(kRowThreads), 0, stream, p, (int)pieces, (int)tokens);
+  return hipGetLastError();
+}
+
 template <int XK, bool W>
 hipError_t launch_rows_w(const RouteQuantArgs& p, hipStream_t stream) {
-  if (p.block_rows == 1) {
-    constexpr int E = unit_of(XK, 1);
-    const int64_t units = p.tokens * (p.cols / E);
-    const int64_t wgs = std::min((units + kRowThreads - 1) / kRowThreads, kMaxWgs);
-    const int64_t pads = std::min<int64_t>((p.rows + kRowThreads - 1) / kRowThreads, kMaxWgs);
-    hipLaunchKernelGGL((route_rows<XK, W>), dim3((unsigned)(wgs + pads)), dim3(kRowThreads), 0, stream, p, units, (unsigned)wgs);
-  } else {
-    const dim3 grid((unsigned)(((p.rows + p.gran - 1) / p.gran) * (p.cols / p.gran)));
-    if (p.gran == 64) hipLaunchKernelGGL((route_blocks<XK, 64, 256, W>), grid, dim3(256), 0, stream, p);
-    else if (p.gran == 128) hipLaunchKernelGGL((route_blocks<XK, 128, 512, W>), grid, dim3(512), 0, stream, p);
-    else hipLaunchKernelGGL((route_blocks<XK, 256, 1024, W>), grid, dim3(1024), 0, stream, p);
-  }
+  const bool four = units_per_lane<unit_of(XK, 1)>(p.tokens, p.cols) == 4;
+  if (p.block_rows == 1) return four ? launch_tokens<XK, W, true, 4>(p, stream) : launch_tokens<XK, W, true, 1>(p, stream);
+  if (by_tokens(p.rows, p.cols)) return four ? launch_tokens<XK, W, false, 4>(p, stream) : launch_tokens<XK, W, false, 1>(p, stream);
+  const dim3 grid((unsigned)(((p.rows + p.gran - 1) / p.gran) * (p.cols / p.gran)));
+  if (p.gran == 64) hipLaunchKernelGGL((route_blocks<XK, 64, 256, W>), grid, dim3(256), 0, stream, p);
+  else if (p.gran == 128) hipLaunchKernelGGL((route_blocks<XK, 128, 512, W>), grid, dim3(512), 0, stream, p);
+  else hipLaunchKernelGGL((route_blocks<XK, 256, 1024, W>), grid, dim3(1024), 0, stream, p);
   return hipGetLastError();
 }
 
@@ -341,7 +518,7 @@ hipError_t launch_rows(const RouteQuantArgs& p, hipStream_t stream) {
 
 // ---- the combine --------------------------------------------------------------
 
-template <int YK, int OK>
+template <int YK, int OK, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void route_combine(const CombineArgs p, int64_t units) {
   constexpr int E = unit_of(YK, OK);
   const int64_t per = p.cols / E;
@@ -356,7 +533,7 @@ __global__ __launch_bounds__(kRowThreads) void route_combine(const CombineArgs p
       if (r < 0 || r >= p.rows) continue;
       const float w = p.weights ? p.weights[t * p.k + j] : 1.0f;
       float y[E];
-      widen_raw(load_raw<YK, E>(p.y, (int64_t)r * p.ldy + c), y);
+      widen_raw(load_raw<YK, E, ONCE>(p.y, (int64_t)r * p.ldy + c), y);
 #pragma unroll
       for (int i = 0; i < E; ++i) acc[i] = __builtin_fmaf(w, y[i], acc[i]);
     }
@@ -374,7 +551,10 @@ template <int YK, int OK>
 hipError_t launch_combine_k(const CombineArgs& p, hipStream_t stream) {
   const int64_t units = p.tokens * (p.cols / unit_of(YK, OK));
   const int64_t wgs = std::min((units + kRowThreads - 1) / kRowThreads, kMaxWgs);
-  hipLaunchKernelGGL((route_combine<YK, OK>), dim3((unsigned)wgs), dim3(kRowThreads), 0, stream, p, units);
+  if (p.tokens * p.k * p.cols * InKind<YK>::kBytes >= kOnceBytes)
+    hipLaunchKernelGGL((route_combine<YK, OK, true>), dim3((unsigned)wgs), dim3(kRowThreads), 0, stream, p, units);
+  else
+    hipLaunchKernelGGL((route_combine<YK, OK, false>), dim3((unsigned)wgs), dim3(kRowThreads), 0, stream, p, units);
   return hipGetLastError();
 }
 
@@ -391,7 +571,7 @@ hipError_t launch_combine_y(const CombineArgs& p, hipStream_t stream) {
 // ---- the gradient of the weights ----------------------------------------------
 
 // A workgroup takes a token, eight of its rows at a time: x once per eight rows.
-template <int XK, int YK>
+template <int XK, int YK, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void route_weight_grad(const WeightGradArgs p) {
   constexpr int E = unit_of(XK, YK), J = 8;
   __shared__ float red[kRowThreads / 64][J];
@@ -413,7 +593,7 @@ __global__ __launch_bounds__(kRowThreads) void route_weight_grad(const WeightGra
         for (int j = 0; j < J; ++j) {
           if (r[j] < 0) continue;
           float y[E];
-          widen_raw(load_raw<YK, E>(p.y, (int64_t)r[j] * p.ldy + c), y);
+          widen_raw(load_raw<YK, E, ONCE>(p.y, (int64_t)r[j] * p.ldy + c), y);
 #pragma unroll
           for (int i = 0; i < E; ++i) acc[j] = __builtin_fmaf(x[i], y[i], acc[j]);
         }
@@ -435,16 +615,24 @@ __global__ __launch_bounds__(kRowThreads) void route_weight_grad(const WeightGra
   }
 }
 
+template <int XK, int YK>
+hipError_t launch_weight_grad_k(const WeightGradArgs& p, hipStream_t stream) {
+  const dim3 grid((unsigned)std::min<int64_t>(p.tokens, kMaxWgs)), block(kRowThreads);
+  if (p.tokens * p.k * p.cols * InKind<YK>::kBytes >= kOnceBytes)
+    hipLaunchKernelGGL((route_weight_grad<XK, YK, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((route_weight_grad<XK, YK, false>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
 template <int XK>
 hipError_t launch_weight_grad_x(const WeightGradArgs& p, hipStream_t stream) {
-  const dim3 grid((unsigned)std::min<int64_t>(p.tokens, kMaxWgs)), block(kRowThreads);
   switch (p.yk) {
-    case 0: hipLaunchKernelGGL((route_weight_grad<XK, 0>), grid, block, 0, stream, p); break;
-    case 1: hipLaunchKernelGGL((route_weight_grad<XK, 1>), grid, block, 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((route_weight_grad<XK, 2>), grid, block, 0, stream, p); break;
+    case 0: return launch_weight_grad_k<XK, 0>(p, stream);
+    case 1: return launch_weight_grad_k<XK, 1>(p, stream);
+    case 2: return launch_weight_grad_k<XK, 2>(p, stream);
     default: return hipErrorInvalidValue;
   }
-  return hipGetLastError();
 }
 
 }  // namespace
@@ -462,7 +650,9 @@ hipError_t launch_sort(const SortArgs& args, hipStream_t stream) {
   return p.wide ? launch_sort_t<int64_t>(p, stream) : launch_sort_t<int32_t>(p, stream);
 }
 
-int64_t route_quant_workspace(int64_t, int64_t, int, int) { return 0; }
+int64_t route_quant_workspace(int64_t tokens, int64_t cols, int64_t rows, int gran, int block_rows) {
+  return block_rows != 1 && by_tokens(rows, cols) ? 4 * (tokens + (rows + gran - 1) / gran) * (cols / gran) : 0;
+}
 
 hipError_t launch_route_quant(const RouteQuantArgs& p, hipStream_t stream) {
   switch (p.xk) {

@@ -81,7 +81,7 @@ int64_t quantize_bytes(int64_t tokens, int64_t cols, int k, int64_t rows, int gr
   if (!good_slots(tokens, k) || !good_dims(tokens, cols) || !good_rows(rows) || !good_gran(gran, cols) ||
       (block_rows != gran && block_rows != 1) || !good_route_blocks(rows, cols, gran, block_rows))
     return DG_EINVAL;
-  return route_quant_workspace(tokens, cols, gran, block_rows);
+  return route_quant_workspace(tokens, cols, rows, gran, block_rows);
 }
 
 int quantize_rows(const void* x, int x_type, int64_t ldx, int64_t tokens, int64_t cols, int k, const int32_t* position,

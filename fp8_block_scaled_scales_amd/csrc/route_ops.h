@@ -76,7 +76,7 @@ struct LoraArgs {
 
 int64_t sort_workspace(int64_t n, int groups);  // bytes; no HIP call
 hipError_t launch_sort(const SortArgs& p, hipStream_t stream);
-int64_t route_quant_workspace(int64_t tokens, int64_t cols, int gran, int block_rows);
+int64_t route_quant_workspace(int64_t tokens, int64_t cols, int64_t rows, int gran, int block_rows);
 hipError_t launch_route_quant(const RouteQuantArgs& p, hipStream_t stream);
 hipError_t launch_combine(const CombineArgs& p, hipStream_t stream);
 hipError_t launch_weight_grad(const WeightGradArgs& p, hipStream_t stream);
