@@ -511,7 +511,8 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
       const v4i val = *reinterpret_cast<const v4i*>(cs + r * LDC + c);
       uint16_t* dst = out + (int64_t)gr * N + gc;
       if (vec_store && gc + 8 <= N) {
-        *reinterpret_cast<v4i*>(dst) = val;
+        if constexpr (DEPTH) __builtin_nontemporal_store(val, reinterpret_cast<v4i*>(dst));
+        else *reinterpret_cast<v4i*>(dst) = val;
       } else {
         for (int t = 0; t < 8 && gc + t < N; ++t) dst[t] = (uint16_t)((uint32_t)val[t >> 1] >> (16 * (t & 1)));
       }
