@@ -29,7 +29,8 @@ namespace {
 constexpr int kMaxGroups = 1024;  // the library's DG_MAX_GROUPS
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
-// Slots that one workgroup sorts alone; beyond, chunks of at least kChunk slots,
+// Slots that one workgroup sorts alone (sort and dispatch of 4096 slots 13.3 us, of
+// 8192 16.0, and in chunks 15.1 and 15.1); beyond, chunks of at least kChunk slots,
 // at most 256 of them, are counted by one launch and placed by a second.
 constexpr int64_t kOneSort = 4096, kChunk = 1024;
 
@@ -286,7 +287,7 @@ __global__ __launch_bounds__(kRowThreads) void route_rows(const RouteQuantArgs p
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       live[u] = piece.col(u, lane) < p.cols;
-      if (live[u]) widen_raw(load_raw<XK, E>(p.x, t * p.ldx + piece.col(u, lane)), x[u]);
+      if (live[u]) widen_raw(load_raw<XK, E, ONCE>(p.x, t * p.ldx + piece.col(u, lane)), x[u]);
     }
     // g x g: the factors of the next of the token's rows are on their way while one is coded
     float s[U], inv[U], s1[U], inv1[U];
@@ -464,16 +465,22 @@ __global__ __launch_bounds__(NT) void route_blocks(const RouteQuantArgs p) {
 
 constexpr int64_t kMaxWgs = 1 << 20;
 
-// g x g blocks of this many codes or more: three launches that read every token
-// twice, instead of one that gathers every row of a block.
-constexpr int64_t kByTokens = 1ll << 23;
+// g x g blocks by tokens: three launches that read every token twice, instead of
+// one that gathers every row of a block (and reads it twice). It pays where a
+// token has several rows and the codes are many. Sort and dispatch of BF16 rows,
+// by tokens / by blocks, in us: 1024 x 8 of 4096 41 / 32, 2048 x 8 of 4096 42 /
+// 48, 8192 x 8 of 4096 109 / 163; 4096 x 2 of 7168 72 / 55, 8192 x 2 of 7168 106 /
+// 94, 4096 x 4 of 7168 80 / 82, 16384 x 2 of 4096 102 / 105.
+constexpr int64_t kByTokens = 1ll << 26;
 
-bool by_tokens(int64_t rows, int64_t cols) { return rows * cols >= kByTokens; }
+bool by_tokens(int64_t tokens, int64_t rows, int64_t cols) { return (rows - tokens) * cols >= kByTokens; }
 
-// Units per lane: four where that leaves the chip enough waves.
+// Units per lane: four where that leaves the chip enough waves (32 a CU). Sort and
+// dispatch to 1 x g, one / four, in us: 1024 x 2 of 4096 in BF16 12.0 / 13.9, 2000 x
+// 2 of 7168 20.2 / 22.5, in FP32 30.9 / 25.5; 8192 x 2 of 4096 to g x g 75 / 67.
 template <int E>
 int units_per_lane(int64_t tokens, int64_t cols) {
-  return cols >= 64 * E * 4 && tokens * (cols / (64 * E * 4)) >= 4096 ? 4 : 1;
+  return cols >= 64 * E * 4 && tokens * (cols / (64 * E * 4)) >= 8192 ? 4 : 1;
 }
 
 template <int XK, bool W, bool OWN, int U>
@@ -492,7 +499,8 @@ hipError_t launch_tokens(const RouteQuantArgs& p, hipStream_t stream) {
     if (err != hipSuccess) return err;
   }
   const dim3 grid((unsigned)(pieces * tokens + pads));
-  if (p.rows * p.cols >= kOnceBytes)
+  // past the caches: 8192 x 8 of 4096 to 1 x g 83 -> 78 us, 2048 x 8 25.1 -> 26.3
+  if (p.rows * p.cols + p.tokens * p.cols * InKind<XK>::kBytes >= 2 * kOnceBytes)
     hipLaunchKernelGGL((route_rows<XK, W, OWN, U, true>), grid, dim3(kRowThreads), 0, stream, p, (int)pieces, (int)tokens);
   else
     hipLaunchKernelGGL((route_rows<XK, W, OWN, U, false>), grid, dim3(kRowThreads), 0, stream, p, (int)pieces, (int)tokens);
@@ -503,7 +511,7 @@ template <int XK, bool W>
 hipError_t launch_rows_w(const RouteQuantArgs& p, hipStream_t stream) {
   const bool four = units_per_lane<unit_of(XK, 1)>(p.tokens, p.cols) == 4;
   if (p.block_rows == 1) return four ? launch_tokens<XK, W, true, 4>(p, stream) : launch_tokens<XK, W, true, 1>(p, stream);
-  if (by_tokens(p.rows, p.cols)) return four ? launch_tokens<XK, W, false, 4>(p, stream) : launch_tokens<XK, W, false, 1>(p, stream);
+  if (by_tokens(p.tokens, p.rows, p.cols)) return four ? launch_tokens<XK, W, false, 4>(p, stream) : launch_tokens<XK, W, false, 1>(p, stream);
   const dim3 grid((unsigned)(((p.rows + p.gran - 1) / p.gran) * (p.cols / p.gran)));
   if (p.gran == 64) hipLaunchKernelGGL((route_blocks<XK, 64, 256, W>), grid, dim3(256), 0, stream, p);
   else if (p.gran == 128) hipLaunchKernelGGL((route_blocks<XK, 128, 512, W>), grid, dim3(512), 0, stream, p);
@@ -551,7 +559,8 @@ template <int YK, int OK>
 hipError_t launch_combine_k(const CombineArgs& p, hipStream_t stream) {
   const int64_t units = p.tokens * (p.cols / unit_of(YK, OK));
   const int64_t wgs = std::min((units + kRowThreads - 1) / kRowThreads, kMaxWgs);
-  if (p.tokens * p.k * p.cols * InKind<YK>::kBytes >= kOnceBytes)
+  // past the caches: 8192 x 8 rows of 4096 in BF16 123 -> 114 us, 1024 x 8 12.8 -> 16.9
+  if (p.tokens * p.k * p.cols * InKind<YK>::kBytes >= 2 * kOnceBytes)
     hipLaunchKernelGGL((route_combine<YK, OK, true>), dim3((unsigned)wgs), dim3(kRowThreads), 0, stream, p, units);
   else
     hipLaunchKernelGGL((route_combine<YK, OK, false>), dim3((unsigned)wgs), dim3(kRowThreads), 0, stream, p, units);
@@ -618,6 +627,8 @@ __global__ __launch_bounds__(kRowThreads) void route_weight_grad(const WeightGra
 template <int XK, int YK>
 hipError_t launch_weight_grad_k(const WeightGradArgs& p, hipStream_t stream) {
   const dim3 grid((unsigned)std::min<int64_t>(p.tokens, kMaxWgs)), block(kRowThreads);
+  // past the caches: with the rows' codes 8192 x 8 of 4096 in BF16 224 -> 203 us, 1024
+  // x 8 45.5 -> 44.1, 512 x 8 34.1 -> 35.7
   if (p.tokens * p.k * p.cols * InKind<YK>::kBytes >= kOnceBytes)
     hipLaunchKernelGGL((route_weight_grad<XK, YK, true>), grid, block, 0, stream, p);
   else
@@ -651,7 +662,7 @@ hipError_t launch_sort(const SortArgs& args, hipStream_t stream) {
 }
 
 int64_t route_quant_workspace(int64_t tokens, int64_t cols, int64_t rows, int gran, int block_rows) {
-  return block_rows != 1 && by_tokens(rows, cols) ? 4 * (tokens + (rows + gran - 1) / gran) * (cols / gran) : 0;
+  return block_rows != 1 && by_tokens(tokens, rows, cols) ? 4 * (tokens + (rows + gran - 1) / gran) * (cols / gran) : 0;
 }
 
 hipError_t launch_route_quant(const RouteQuantArgs& p, hipStream_t stream) {
