@@ -1,7 +1,12 @@
 // The products of groups of rows (gemm_groups.h), out rows of group e = act(A
 // rows of group e times B_e^T) with the pre-activation where it is kept: the
 // streaming, 64x64 and tiled entries, B stored [N,K] or [K,N]; the 256-row
-// entries are in gemm_fp8_grouped_big.hip.
+// entries are in gemm_fp8_grouped_big.hip. One launch for all groups: their
+// tiles fill the chip together, where a launch per group would leave most CUs
+// idle (64 groups of 8 rows, 4096 x 2048: 95 us in one, of which reading the
+// 537 MB of weights takes 92 at the rate of a copy). With few rows per group the
+// weights' bytes bound it; the 128x128 tile streams them best (forced: 32x32 165 us,
+// 64x64 152, 256x256 132), although its rows are mostly empty there.
 
 #include <hip/hip_runtime.h>
 

@@ -106,7 +106,8 @@ __device__ __forceinline__ bool find_tile(const RowGroups& g, int tiles_n, Group
 // For DepthGroups: every group has the same tiles_m x tiles_n tiles, and each
 // XCD takes an eighth of every group's raster, since a group's length is the
 // work of its tiles: whole groups per XCD would leave the XCDs of short groups
-// idle.
+// idle. Where a group has too few tiles for every XCD, the next group begins
+// with those that had none.
 __host__ __device__ constexpr int64_t depth_tiles_per_xcd(int64_t tiles) { return (tiles + 7) / 8; }
 
 template <int GROUP_M>
@@ -114,7 +115,8 @@ __device__ __forceinline__ bool find_tile(const DepthGroups& g, int tiles_m, int
   const int tiles = tiles_m * tiles_n, per = (int)depth_tiles_per_xcd(tiles);
   const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
   t.group = local / per;
-  const int in = xcd * per + local % per;
+  const int used = (tiles + per - 1) / per;
+  const int in = ((xcd + t.group * used) & 7) * per + local % per;
   if (in >= tiles || t.group >= g.n) return false;
   const int strip = GROUP_M * tiles_n;
   const int first = in / strip * GROUP_M, high = min(tiles_m - first, GROUP_M), rest = in % strip;

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 
 #include "../../include/dg.h"
@@ -218,14 +219,26 @@ int64_t row_grid(const KernelEntry* e, int64_t rows, int groups, int64_t N) {
   return (rows / e->bm + std::min<int64_t>(groups, rows)) * cdiv(N, e->bn);
 }
 
-// Estimated time as the plain products' (estimate_us in dg_host.hip), with every
-// group of the mean length.
+// Estimated time as the plain products' (estimate_us in dg_host.hip), for lengths
+// that the host does not know: rows that each fall to any group leave so many of
+// them live, and a live group is taken to be longer than n rows with the chance
+// exp(-n / mean), which gives it 1 / (1 - exp(-bm / mean)) tile rows; and half a
+// round more where there is more than one, since not all workgroups end
+// together. A live group's weights come from HBM (5.3 TB/s) at least once: of the
+// entries that this holds back alike the table's first, 128x128, is taken (200
+// rows in 16 groups, 8192 x 8192: 193 us, 32x32 tiles 231; but 8 rows in 8 groups,
+// 4096 x 7168: 56 and 34, the estimate's choice). On 23 shapes, 16 to 8192 tokens
+// with 2 to 8 rows each in 8 to 64 groups, N and K 1024 to 8192, the entry of the
+// least estimate took 1.7% longer than the fastest on average and 12% at most; with
+// every group of the mean length and whole rounds 4.8% and 55%.
 double estimate_groups(const KernelEntry* e, int64_t rows, int groups, int64_t N, int64_t K) {
-  const int64_t live = std::min<int64_t>(groups, rows);
-  const int64_t rounds = cdiv(live * cdiv(cdiv(rows, live), e->bm) * cdiv(N, e->bn), 256);
+  const double live = -groups * std::expm1((double)rows * std::log1p(-1.0 / groups));
+  const double tiles = live / -std::expm1(-e->bm * live / (double)rows) * (double)cdiv(N, e->bn);
+  const double rounds = tiles <= 256.0 ? 1.0 : tiles / 256.0 + 0.5;
   const double bytes = (double)(e->bm + e->bn) * (double)K;
   const double flop = 2.0 * e->bm * e->bn * (double)K;
-  return e->launch_us + (double)rounds * (e->round_us + std::max(bytes / (e->cu_gbps * 1e3), flop / (e->cu_tflops * 1e6)));
+  const double tiled = e->launch_us + rounds * (e->round_us + std::max(bytes / (e->cu_gbps * 1e3), flop / (e->cu_tflops * 1e6)));
+  return std::max(tiled, live * (double)N * (double)K / 5.3e6);
 }
 
 // Threads of a launch of e: grids are limited to less than 2^32 of them.
@@ -300,11 +313,15 @@ int grouped(const void* a, const void* b, const float* sa, const float* sb, cons
   return done(launch_grouped(pl.e->id, p, RowGroups{offsets, groups, (int)rows}, pl.grid, static_cast<hipStream_t>(stream)));
 }
 
-// 256x256 tiles where they are enough to fill the CUs, else 128x128.
+// 256x256 tiles where every CU gets two of them, else 128x128. 256 / 128, in us: 8
+// groups of 2000 x 2 rows, 1024 x 512 (64 tiles of 256) 21.7 / 14.5, 2048 x 1024 (256)
+// 23.8 / 27.4, 4096 x 2048 (1024) 69 / 98; 64 groups of 8192 x 2 rows, 512 x 512 (256)
+// 36.3 / 26.7, 768 x 512 (384) 38 / 32, 1024 x 512 (512) 40.2 / 39.7; 8 groups of 500 x
+// 2 rows, 4096 x 2048 43.7 / 55.8.
 GroupPlan plan_depth(int64_t M, int64_t N, int groups, int sgran) {
   const int gran = kernel_gran(sgran), force = forced_tile();
   GroupPlan p{nullptr, 0};
-  const int want = cdiv(M, 256) * cdiv(N, 256) * groups >= 256 ? (gran == 128 ? 4 : 5) : (gran == 128 ? 0 : 1);
+  const int want = cdiv(M, 256) * cdiv(N, 256) * groups >= 512 ? (gran == 128 ? 4 : 5) : (gran == 128 ? 0 : 1);
   for (int i = 0; i < kTableSize; ++i) {
     const KernelEntry* e = &kTable[i];
     if (e->gran != gran || (e->id != 0 && e->id != 1 && e->id != 4 && e->id != 5)) continue;
