@@ -82,10 +82,10 @@ DEFAULT_WORKLOAD = 4      # large square M=N=K=8192, g=128: the largest shape, M
 # workload runs (KERNEL_SOURCES) as they were when the counters were taken. A
 # different hash means the kernel changed since: traffic is null.
 TRAFFIC = {
-    "square8192": {"src": "91c467ea0331ea9b", "bytes": 940634079},
-    "prefill_m4096_n7168_k2048": {"src": "91c467ea0331ea9b", "bytes": 151252041},
-    "longk_m2000_n4000_k16384_g64": {"src": "91c467ea0331ea9b", "bytes": 278792815},
-    "decode_m64_n4096_k7168": {"src": "6af1a50332b82008", "bytes": 33667236},
+    "square8192": {"src": "50fbd06ee289c5e8", "bytes": 940760596},
+    "prefill_m4096_n7168_k2048": {"src": "50fbd06ee289c5e8", "bytes": 151255113},
+    "longk_m2000_n4000_k16384_g64": {"src": "50fbd06ee289c5e8", "bytes": 278793167},
+    "decode_m64_n4096_k7168": {"src": "a0547f648979db4a", "bytes": 33667236},
 }
 
 # What makes up each workload's kernel: the unit that compiles its class, the

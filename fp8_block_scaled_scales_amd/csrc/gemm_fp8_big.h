@@ -511,6 +511,7 @@ __global__ __launch_bounds__(NT) void gemm_fp8_nt_big(const uint8_t* __restrict_
       const v4i val = *reinterpret_cast<const v4i*>(cs + r * LDC + c);
       uint16_t* dst = out + (int64_t)gr * N + gc;
       if (vec_store && gc + 8 <= N) {
+        // the weights' gradients of many groups are more than the caches hold (1.07 GB: 734 -> 701 us)
         if constexpr (DEPTH) __builtin_nontemporal_store(val, reinterpret_cast<v4i*>(dst));
         else *reinterpret_cast<v4i*>(dst) = val;
       } else {
