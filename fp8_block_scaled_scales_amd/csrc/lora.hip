@@ -318,7 +318,13 @@ __device__ __forceinline__ void copy_row(const LoraArgs& p, int64_t tok, int lan
   }
 }
 
-// f as TERMS 16-bit numbers: its rounding, that of the rest, ...
+__device__ __forceinline__ float rest_of(float f, float h) {
+  const float r = f - h;
+  return r == r ? r : 0.0f;
+}
+
+// f as TERMS 16-bit numbers: its rounding, that of the rest, ... (an infinite one
+// has no rest)
 template <int XK, int TERMS>
 __device__ __forceinline__ void split16(float f, uint16_t (&t)[TERMS]) {
 #pragma unroll
@@ -326,11 +332,11 @@ __device__ __forceinline__ void split16(float f, uint16_t (&t)[TERMS]) {
     if constexpr (XK == 1) {
       const __bf16 h = (__bf16)f;
       t[i] = __builtin_bit_cast(uint16_t, h);
-      f -= (float)h;
+      f = rest_of(f, (float)h);
     } else {
       const _Float16 h = (_Float16)f;
       t[i] = __builtin_bit_cast(uint16_t, h);
-      f -= (float)h;
+      f = rest_of(f, (float)h);
     }
   }
 }
@@ -422,7 +428,9 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
       for (int e = 0; e < 4; ++e) v[i][e] *= scale;
       float down = 1.0f;
       if constexpr (XK == 2) {
-        float top = amax4(v[i]);
+        float top = 0.0f;  // of those that are finite
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[i][e]) < __builtin_inff() ? fabsf(v[i][e]) : 0.0f);
 #pragma unroll
         for (int d = 1; d < FOURS; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
         const int e = min(max(__builtin_amdgcn_frexp_expf(top), -100), 100);

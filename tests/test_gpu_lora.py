@@ -121,3 +121,46 @@ def test_indices_outside_are_not_followed(dg):
         dg.dg_lora(x.to(DEV), a.to(DEV), b.to(DEV), torch.tensor(wild, dtype=torch.int32, device=DEV), pos, bad, base=base.to(DEV), out=guard[10 : 10 + tokens])
         torch.cuda.synchronize()
         assert (guard[:10] == -9.0).all() and (guard[10 + tokens :] == -9.0).all()
+
+
+@pytest.mark.parametrize("xk", [BF16, F16])
+@pytest.mark.parametrize("tokens,K", [(6, 64), (300, 72)])
+def test_infinities(dg, tokens, K, xk):
+    """A row whose products with A overflow has the infinities of the formula, beside finite ones; other rows are untouched."""
+    x, a, b = torch.ones(tokens, K, dtype=xk), torch.zeros(2, 16, K, dtype=xk), torch.ones(2, 40, 16, dtype=xk)
+    a[0, 0, 0], a[0, 1, 1], a[1, 3, 2] = 2.0, -3.0, 1.0
+    b[0, ::2, 0] = -1.0
+    b[0, :, 1] = 0.5
+    x[2, 0], x[2, 1] = float("inf"), 60000.0  # v: infinite at rank 0, large at rank 1
+    x[3, 4] = float("nan")  # times zeros of A: NaN
+    ids = (torch.arange(tokens) % 2).to(torch.int32)[:, None]
+    ids[4] = -1
+    x[4] = float("nan")  # without an adapter: not read
+    base = torch.ones(tokens, 40, dtype=F32)
+    off, pos, slot = dg.dg_route_sort(ids.to(DEV), 2)
+    say("infinities %d %s" % (tokens, xk))
+    out = dg.dg_lora(x.to(DEV), a.to(DEV), b.to(DEV), off, pos, slot, None, base.to(DEV)).cpu()
+    want = base.double().clone()
+    for t in range(tokens):
+        if ids[t, 0] >= 0:
+            e = int(ids[t, 0])
+            # a rank's product is over the x that its row of A names, but for NaN and infinities times zero
+            want[t] += b[e].double() @ (a[e].double() @ x[t].double())
+    # an infinite x times the zeros of A's other rows makes those ranks NaN in the formula too
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(torch.isinf(out), torch.isinf(want))
+    fine = torch.isfinite(want)
+    assert ((out.double() - want).abs()[fine] <= 2.0 ** -20 * want.abs()[fine]).all()
+
+
+def test_products_past_fp32(dg):
+    """v = x A^T past FP32's range without an infinite operand: infinities of the right sign in out."""
+    x, a = torch.zeros(5, 64, dtype=BF16), torch.zeros(1, 8, 64, dtype=BF16)
+    x[:, 0], x[:, 1], a[0, 0, 0], a[0, 1, 1] = 3e38, 2.0, 4.0, 1.0
+    x[1, 0], x[2, 0] = 1.0, -3e38
+    b = torch.ones(1, 24, 8, dtype=BF16)
+    b[0, :, 1] = -1e30
+    off, pos, slot = dg.dg_route_sort(torch.zeros(5, 1, dtype=torch.int32, device=DEV), 1)
+    say("products past FP32")
+    for ok in (BF16, F32):
+        out = dg.dg_lora(x.to(DEV), a.to(DEV), b.to(DEV), off, pos, slot, None, torch.zeros(5, 24, dtype=ok, device=DEV)).cpu().float()
+        assert (out[[0, 3, 4]] == float("inf")).all() and (out[2] == -float("inf")).all() and torch.isfinite(out[1]).all()

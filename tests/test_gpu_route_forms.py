@@ -107,6 +107,40 @@ def test_large_combine_and_weight_grad(dg, tokens, k, cols, yk, ok):
     assert ((dw.double() - wdw).abs() <= (cols / 256 + 20) * ref.U32 * sdw + ref.U32 * wdw.abs()).all()
 
 
+@pytest.mark.parametrize("tokens,k,cols,g", [(50, 3, 1024, 128), (50, 3, 1024, 64), (40, 5, 512, 256), (1100, 11, 6400, 128)])
+@pytest.mark.parametrize("xk", [BF16, F32])
+def test_infinities_and_nan(dg, tokens, k, cols, g, xk):
+    """Codes and factors are the quantisers' on the gathered matrix with infinities and NaN of both signs in it and in the
+    weights, in one block or row alone and beside finite values; in tokens that no group takes they change nothing."""
+    ids = rr.routing(tokens, tokens, k, 6, idle=0.1)
+    ids[7] = -1
+    x = normal(tokens, tokens, cols)
+    x[3, 5], x[4, 70], x[5, 0], x[6, 9], x[7] = float("inf"), float("-inf"), float("nan"), -float("nan"), float("nan")
+    x[8], x[9] = float("nan"), float("inf")
+    x = x.to(xk)
+    w = normal(9, tokens, k)
+    w[3, 0], w[10, 0], w[11, 1], w[12, 0], w[9, 0] = 0.0, float("inf"), float("nan"), float("-inf"), 0.0
+    off, pos, slot = dg.dg_route_sort(ids.to(DEV), 6, g)
+    end = int(off[-1])
+    at = slot[:end].long()
+    for weights in (None, w):
+        v = x[at.clamp(min=0) // k].float()
+        if weights is not None:
+            v *= w.reshape(-1)[at.clamp(min=0)][:, None]
+        v[at < 0] = 0.0
+        for fmt in (0, 1):
+            say("infinities %dx%d cols %d g=%d %s weights=%d fmt=%d" % (tokens, k, cols, g, xk, weights is not None, fmt))
+            for br, plain in ((1, dg.dg_quantize_fp8_rows), (g, dg.dg_quantize_fp8_blocks)):
+                q, s = dg.dg_route_quantize_fp8(x, pos, slot, weights, gran=g, block_rows=br, fmt=fmt)
+                wq, ws = plain(v, gran=g, fmt=fmt)
+                dt = (torch.float8_e4m3fn, torch.float8_e5m2)[fmt]
+                got, want = q[:end].view(dt).float(), wq.view(dt).float()
+                # a NaN's sign is not held to anything
+                assert torch.equal(torch.isnan(got), torch.isnan(want))
+                assert torch.equal(torch.where(torch.isnan(want), 0, q[:end]), torch.where(torch.isnan(want), 0, wq))
+                assert torch.equal(torch.nan_to_num(s[: ws.shape[0]], 7.0, 8.0), torch.nan_to_num(ws, 7.0, 8.0))
+
+
 # ---- every call at once --------------------------------------------------------------
 
 
