@@ -333,3 +333,61 @@ def test_lora_race_check_build(dg, tokens, groups, N, K, rank, xk):
     say("adapters' race check %d tokens N %d K %d rank %d %s" % (tokens, N, K, rank, xk))
     _both(dg, (out,), lambda lib: lib.dg_lora(p(x), kind, K, tokens, K, p(a), p(b), p(scale), N, rank, groups, p(off), p(pos), p(slot),
                                               p(base), N, p(out), 0, p(ws), nb, st))
+
+
+# ---- offsets past 32 bits ----------------------------------------------------------------
+
+
+def test_products_past_32_bits(dg):
+    """Weights of more than 2^32 codes and gradients of more than 2^32 elements: the last groups against the plain calls."""
+    groups, N, K, g = 300, 4096, 4096, 128
+    assert groups * N * K > 1 << 32
+    b = torch.randint(0, 96, (groups, N, K), dtype=torch.uint8, device=DEV)
+    sb = torch.rand(groups, N // g, K // g, device=DEV)
+    off = torch.zeros(groups + 1, dtype=torch.int32, device=DEV)
+    off[-2], off[-1] = 128, 384  # the last two groups' rows, the others have none
+    q, s = dg.dg_quantize_fp8_blocks(normal(1, 384, K), gran=g)
+    say("groups of %d codes" % b.numel())
+    out = dg.dg_gemm_fp8_grouped(q, b, s, sb, off, gran=g)
+    back = dg.dg_gemm_fp8_grouped(q, b, s, sb.transpose(1, 2).contiguous(), off, gran=g, layout=dg.DG_LAYOUT_NN)
+    for e, lo, hi in ((groups - 2, 0, 128), (groups - 1, 128, 384)):
+        at, sat = q[lo:hi], s[lo // g : hi // g]
+        for got, want in ((out, dg.dg_gemm_fp8_layout(at, b[e], sat, sb[e], gran=g)),
+                          (back, dg.dg_gemm_fp8_layout(at, b[e], sat, sb[e].t().contiguous(), gran=g, layout=dg.DG_LAYOUT_NN))):
+            # the plain call may run another tile: the FP32 sums' order differs
+            w = want.float()
+            assert float((got[lo:hi].float() - w).norm() / w.norm()) <= 2.0 ** -8
+    del b, sb
+    d, sd = dg.dg_quantize_fp8_blocks(normal(2, 384, N), gran=g)
+    dw = dg.dg_gemm_fp8_grouped_wgrad(d, q, sd, s, off, gran=g, fmt_a=0)
+    assert not dw[: groups - 2].any()
+    for e, lo, hi in ((groups - 2, 0, 128), (groups - 1, 128, 384)):
+        want = dg.dg_gemm_fp8_layout(d[lo:hi], q[lo:hi], sd[lo // g : hi // g].t().contiguous(), s[lo // g : hi // g].t().contiguous(), gran=g,
+                                     layout=dg.DG_LAYOUT_TN).float()
+        assert float((dw[e].float() - want).norm() / want.norm()) <= 2.0 ** -8
+
+
+def test_adapters_past_32_bits(dg):
+    """A and B of more than 2^32 bytes, a base whose rows span more than 2^32 elements: the last rows."""
+    groups, rank, K = 1024, 128, 18432
+    a = torch.zeros(groups, rank, K, dtype=BF16, device=DEV)
+    assert a.numel() * 2 > 1 << 32
+    a[-1] = normal(1, rank, K, dtype=BF16)
+    b = torch.zeros(groups, K, rank, dtype=BF16, device=DEV)
+    b[-1] = normal(2, K, rank, dtype=BF16)
+    tokens = 70000
+    ids = torch.full((tokens, 1), -1, dtype=torch.int32, device=DEV)
+    ids[:40], ids[-3:] = 5, groups - 1
+    base = normal(3, tokens, 16, dtype=BF16).repeat(1, 4096)  # [tokens, 65536]
+    off, pos, slot = dg.dg_route_sort(ids, groups)
+    x = torch.zeros(tokens, K, dtype=BF16, device=DEV)
+    x[-3:] = normal(4, 3, K, dtype=BF16)
+    say("adapters of %d elements" % a.numel())
+    out = dg.dg_lora(x, a, b, off, pos, slot, None, base[:, :K])
+    v = x[-3:].double() @ a[-1].double().t()
+    want = base[-3:, :K].double() + v @ b[-1].double().t()
+    size = base[-3:, :K].double().abs() + x[-3:].double().abs() @ a[-1].double().abs().t() @ b[-1].double().abs().t()
+    # FP32 sums of K and of rank terms, v as two BF16 numbers (2^-16 of it), one rounding
+    room = (ref.half_step(BF16) * want.abs() + ((K + rank) * ref.U32 + 2.0 ** -16) * size) * 1.01
+    assert ((out[-3:].double() - want).abs() <= room).all()
+    assert torch.equal(out[:-3], base[:-3, :K])
