@@ -197,12 +197,36 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
   return __builtin_fmaf(-__builtin_fmaf(q, s, -x), inv, q);
 }
 
+// The same in three, for BF16 and FP16 values and the factor of their own block's
+// largest: one correction gives RN(x / s) for each of the 2^20 pairs of mantissas
+// of x and of the largest value (all tried; the largest finite value of either
+// format is 7 times a power of two). The exponents play no part while the
+// remainder, down to 2^-48 of an x that does not code to zero, stays normal: s
+// from 2^-60 to 2^60. (Coding x m (1 - e) and x m (1 + e) instead, m = w / s, and
+// dividing where the codes differ: 85 us of 94 with weights, but 127 of 78 without,
+// where exact ties are common.)
+__device__ __forceinline__ float quotient_of_block(float x, float s, float inv) {
+  const float q = x * inv;
+  return __builtin_fmaf(-__builtin_fmaf(q, s, -x), inv, q);
+}
+
 // A wave whose factors all have normal reciprocals divides by them; where one has
-// not, every lane of it takes the quantisers' two ways (the same codes).
-template <int FMT, int E>
+// not, every lane of it takes the quantisers' two ways (the same codes). SHORT:
+// quotient_of_block's values.
+template <int FMT, bool SHORT, int E>
 __device__ __forceinline__ void codes_fmt(const float (&y)[E], float s, float inv, int (&c)[E / 4]) {
   const bool fast = recip_ok(s);
-  if (__all(fast)) {
+  if constexpr (SHORT) {
+    if (__all(s >= 0x1p-60f && s <= 0x1p60f)) {
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        const int lo = cvt2<FMT, false>(quotient_of_block(y[4 * i], s, inv), quotient_of_block(y[4 * i + 1], s, inv), 0);
+        c[i] = cvt2<FMT, true>(quotient_of_block(y[4 * i + 2], s, inv), quotient_of_block(y[4 * i + 3], s, inv), lo);
+      }
+      return;
+    }
+  }
+  if (!SHORT && __all(fast)) {
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
       const int lo = cvt2<FMT, false>(quotient(y[4 * i], s, inv), quotient(y[4 * i + 1], s, inv), 0);
@@ -218,11 +242,11 @@ __device__ __forceinline__ void codes_fmt(const float (&y)[E], float s, float in
   }
 }
 
-// The codes of y / s, inv = 1 / s.
-template <int E>
+// The codes of y / s, inv = 1 / s. SHORT: y as it was read, of 16 bits.
+template <bool SHORT, int E>
 __device__ __forceinline__ void codes_of(const float (&y)[E], float s, float inv, int fmt, int (&c)[E / 4]) {
-  if (fmt == 1) codes_fmt<1>(y, s, inv, c);
-  else codes_fmt<0>(y, s, inv, c);
+  if (fmt == 1) codes_fmt<1, SHORT>(y, s, inv, c);
+  else codes_fmt<0, SHORT>(y, s, inv, c);
 }
 
 template <bool ONCE, int E>
@@ -267,8 +291,9 @@ struct Piece {
 // columns. OWN: 1 x g, the factors are the token's own segments' (with weights:
 // each row's, since |w x| is largest where |x| is: rounding keeps order);
 // otherwise the factors of g x g blocks are in scales already. Sorted rows taken
-// by their own waves instead would read x k times. 78 us (0.34 GB: 57; 72 vector
-// instructions per lane and eight codes fill 82% of the cycles), with weights 94; 1 x
+// by their own waves instead would read x k times. 69 us (0.34 GB: 57; with two
+// corrections of every quotient 78, the vector ALU busy 84% of the cycles), with
+// weights, whose quotients need both, 94; 1 x
 // g, 2000 x 2 rows of 7168 in FP32 with weights 27 to 34 (86 MB: 15; one round of
 // waves, whose loads nothing overlaps; sharing the factors' divisions over a
 // segment's lanes took as long).
@@ -317,7 +342,7 @@ __global__ __launch_bounds__(kRowThreads) void route_rows(const RouteQuantArgs p
         top[u] = segment_max<E>(amax_of(x[u]), p.gran);
         if constexpr (!W) {
           own[u] = block_scale(top[u], fmax);
-          codes_of(x[u], own[u], 1.0f / own[u], p.fmt, code[u]);
+          codes_of<XK != 0>(x[u], own[u], 1.0f / own[u], p.fmt, code[u]);
         }
       }
     }
@@ -349,7 +374,7 @@ __global__ __launch_bounds__(kRowThreads) void route_rows(const RouteQuantArgs p
             s[u] = block_scale(fabsf(top[u] * w), fmax);
             inv[u] = 1.0f / s[u];
           }
-          codes_of(y, s[u], inv[u], p.fmt, code[u]);
+          codes_of<XK != 0 && !W>(y, s[u], inv[u], p.fmt, code[u]);
         } else {
           s[u] = own[u];
         }
@@ -467,7 +492,7 @@ __global__ __launch_bounds__(NT) void route_blocks(const RouteQuantArgs p) {
     const int64_t r = rb * G + i * RPP + rsub;
     if (r < p.rows && p.slot[r] != -2) {
       int code[E / 4];
-      codes_of(z[i], s, inv, p.fmt, code);
+      codes_of<XK != 0 && !W>(z[i], s, inv, p.fmt, code);
       put_codes<false, E>(p.q + r * p.cols + c, code);
     }
   }
