@@ -32,7 +32,7 @@ struct RouteQuantArgs {
   int64_t rows;
   uint8_t* q;
   float* scales;
-  float* ws;  // g x g blocks: every token's segment maxima (route_quant_workspace bytes)
+  float* ws;  // g x g blocks by tokens: their segment maxima, then the blocks' reciprocal factors (route_quant_workspace bytes)
   int gran, block_rows, fmt, xk;
 };
 
