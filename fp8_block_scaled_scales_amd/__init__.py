@@ -849,7 +849,7 @@ def dg_route_sort(ids, groups: int, align: int = 1, offsets=None, position=None,
     dev = ids.device
     _check(ids, "ids", tuple(_ID_BYTES), shape, dev)
     least = _count(_lib.dg_route_rows(tokens, k, groups, align), "dg_route_sort")
-    if slot is not None and (slot.dim() != 1 or slot.shape[0] < least):
+    if slot is not None and (not isinstance(slot, torch.Tensor) or slot.dim() != 1 or slot.shape[0] < least):
         raise ValueError("slot must be 1-D with at least dg_route_rows(...) = %d entries" % least)
     rows = least if slot is None else slot.shape[0]
     offsets = _out(offsets, "offsets", _I32, (groups + 1,), dev, stream)
@@ -953,8 +953,8 @@ def dg_route_combine(y, position, weights=None, res=None, out=None, stream=None)
     if weights is not None:
         _check(weights, "weights", _F32, (tokens, k), dev)
     ldy = _rows(y, "y", _IN_OF, (rows, cols), dev)
-    kinds = (res.dtype,) if res is not None else (out.dtype,) if isinstance(out, torch.Tensor) else (y.dtype,)
     ldres = 0 if res is None else _rows(res, "res", tuple(_IN_OF), (tokens, cols), dev)
+    kinds = (res.dtype,) if res is not None else (out.dtype,) if isinstance(out, torch.Tensor) else (y.dtype,)
     if kinds[0] not in _IN_OF:
         raise ValueError("out must be float32, bfloat16 or float16")
     out = _out(out, "out", kinds, (tokens, cols), dev, stream)

@@ -299,3 +299,15 @@ def test_references_against_differences():
         d[r, 3] = 1.0
         assert abs(loss(w, y + d) - loss(w, y) - float(dy[r, 3])) <= 1e-6
     assert ref.U32 == rr.U32
+
+
+def test_things_that_are_no_tensors(dg):
+    z = torch.zeros
+    x, pos, slot, off = z(4, 256, dtype=torch.bfloat16), z(4, 2, dtype=torch.int32), z(16, dtype=torch.int32), z(4, dtype=torch.int32)
+    for fn in (lambda: dg.dg_route_sort([[0, 1]], 3), lambda: dg.dg_route_sort(pos, 3, slot=[0] * 8), lambda: dg.dg_route_sort(pos, 3, offsets=[0]),
+               lambda: dg.dg_route_quantize_fp8(x, pos, [0] * 8), lambda: dg.dg_route_quantize_fp8(x, pos, None), lambda: dg.dg_route_quantize_fp8(x, None, slot),
+               lambda: dg.dg_route_combine(x, pos, [1.0]), lambda: dg.dg_route_combine(x, pos, None, 1.0), lambda: dg.dg_route_combine(x, pos, out=1.0),
+               lambda: dg.dg_route_weight_grad(x, None, pos), lambda: dg.dg_gemm_fp8_grouped(x, 1, x, x, off), lambda: dg.dg_lora(x, 1, 1, off, pos, slot),
+               lambda: dg.dg_lora(x, x, x, None, pos, slot)):
+        with pytest.raises((TypeError, ValueError)):
+            fn()
