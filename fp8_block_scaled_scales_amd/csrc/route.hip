@@ -261,10 +261,15 @@ __device__ __forceinline__ void put_codes(uint8_t* q, const int (&c)[E / 4]) {
 }
 
 // Rows between a group's last and the next group: codes of zero and, with a
-// factor per row, factors of one. A wave looks at 64 rows.
+// factor per row, factors of one. A wave looks at kPadRows rows. 8 / 64 of them, in
+// us: 4 x 6 of 7168 to 19 groups of 128 rows with the weights' gradient 14.5 / 31.2, 81 x
+// 2 of 1280 to 44 of 16 10.8 / 15.3, 8192 x 8 of 4096 to 64 of 128 80 / 89, of 1 77.5 /
+// 77.8; 65536 x 8 of 256 72 / 69.
+constexpr int kPadRows = 8;
+
 __device__ __forceinline__ void pad_rows(const RouteQuantArgs& p, int64_t wave, int lane) {
-  const int64_t r0 = wave * 64;
-  const int s = r0 + lane < p.rows ? p.slot[r0 + lane] : -2;
+  const int64_t r0 = wave * kPadRows;
+  const int s = lane < kPadRows && r0 + lane < p.rows ? p.slot[r0 + lane] : -2;
   uint64_t m = __ballot(s == -1);
   const int64_t segs = p.cols / p.gran;
   while (m) {
@@ -304,7 +309,7 @@ __global__ __launch_bounds__(kRowThreads) void route_rows(const RouteQuantArgs p
   const int unit_wgs = pieces * token_wgs;
   if ((int)blockIdx.x >= unit_wgs) {
     const int64_t first = (int64_t)((int)blockIdx.x - unit_wgs) * kRowWaves + wave, step = (int64_t)((int)gridDim.x - unit_wgs) * kRowWaves;
-    for (int64_t w = first; w * 64 < p.rows; w += step) pad_rows(p, w, lane);
+    for (int64_t w = first; w * kPadRows < p.rows; w += step) pad_rows(p, w, lane);
     return;
   }
   const Piece<E, U> piece{(int64_t)((int)blockIdx.x % pieces) * (64 * E * U)};
@@ -523,7 +528,7 @@ hipError_t launch_tokens(const RouteQuantArgs& p, hipStream_t stream) {
   constexpr int E = unit_of(XK, 1);
   const int64_t pieces = (p.cols + 64 * E * U - 1) / (64 * E * U);
   const int64_t tokens = std::min((p.tokens + kRowWaves - 1) / kRowWaves, std::max<int64_t>(1, kMaxWgs / pieces));
-  const int64_t pads = std::min<int64_t>((p.rows + kRowThreads - 1) / kRowThreads, kMaxWgs);
+  const int64_t pads = std::min<int64_t>((p.rows + kRowWaves * kPadRows - 1) / (kRowWaves * kPadRows), kMaxWgs);
   if constexpr (!OWN) {
     hipLaunchKernelGGL((route_maxima<XK, U>), dim3((unsigned)(pieces * tokens)), dim3(kRowThreads), 0, stream, p, (int)pieces, (int)tokens);
     hipError_t err = hipGetLastError();
