@@ -299,9 +299,9 @@ struct Piece {
 // by their own waves instead would read x k times. 69 us (0.34 GB: 57; with two
 // corrections of every quotient 78, the vector ALU busy 84% of the cycles), with
 // weights, whose quotients need both, 94; 1 x
-// g, 2000 x 2 rows of 7168 in FP32 with weights 27 to 34 (86 MB: 15; one round of
-// waves, whose loads nothing overlaps; sharing the factors' divisions over a
-// segment's lanes took as long).
+// g, 2000 x 2 rows of 7168 in FP32 with weights 22 (86 MB: 15; 33 while a wave cleared
+// up to 64 rows between groups; sharing the factors' divisions over a segment's
+// lanes changed nothing).
 template <int XK, bool W, bool OWN, int U, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void route_rows(const RouteQuantArgs p, int pieces, int token_wgs) {
   constexpr int E = unit_of(XK, 1);
