@@ -21,8 +21,11 @@
 // numbers (its rounding and that of the rest, 16 bits of BF16 or 22 of FP16),
 // three where the operands are BF16 and out is FP32: rounding it once would
 // cost up to 2^-9 of every term, as much as a BF16 out's own rounding where the
-// base is small. FP16 rows are scaled by a power of two first, so that no v
-// overflows. The sum with base is FP32, rounded once.
+// base is small. FP16 rows are scaled by a power of two first, to a largest v in
+// [2^14, 2^15): none overflows, and the rest of a small one keeps FP16's whole
+// range below it (2^-25 is half its smallest step, 2^-39 of the row's largest: 22
+// bits of a v down to 2^-17 of that, 16 at 2^-23). The sum with base is FP32,
+// rounded once.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -434,8 +437,8 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
 #pragma unroll
         for (int d = 1; d < FOURS; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
         const int e = min(max(__builtin_amdgcn_frexp_expf(top), -100), 100);
-        down = __builtin_amdgcn_ldexpf(1.0f, -e);
-        if (n == 0 && m < BM) back[m] = __builtin_amdgcn_ldexpf(1.0f, e);
+        down = __builtin_amdgcn_ldexpf(1.0f, 15 - e);  // rank 128 and B at its largest: sums below 2^39
+        if (n == 0 && m < BM) back[m] = __builtin_amdgcn_ldexpf(1.0f, e - 15);
       }
       if (m < BM) {
         uint16_t f[4][TERMS];

@@ -674,8 +674,9 @@ int dg_gemm_fp8_grouped_wgrad(const void* a, const void* b, const float* sa, con
  *
  * for rows sorted by adapter with dg_route_sort (k = 1, align = 1, rows =
  * tokens; once for all projections of a step). A row without an adapter is base
- * alone. Sums in FP32; x A^T enters the second product with at least 16 bits; one
- * rounding at the end.
+ * alone. Sums in FP32; an element of x A^T enters the second product with at least
+ * 16 bits (with FP16 operands one below 2^-23 of its row's largest to within 2^-39
+ * of that); one rounding at the end.
  *
  *   x        [tokens][K] of type DG_IN_BF16 or DG_IN_F16, row pitch ldx.
  *   a, b     [groups][rank][K] and [groups][N][rank] of x's type.

@@ -1,0 +1,64 @@
+"""The adapters where their numbers end: elements of a row far below its largest,
+products and scales near FP32's ends, positions outside the rows, infinities in B."""
+
+import pytest
+import torch
+
+from tests import _layer_ref as ref
+from tests._gpu import say
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def dg():
+    import fp8_block_scaled_scales_amd as dg
+
+    return dg
+
+
+def mantissas(seed, *shape):
+    """Numbers of 11 bits in [1, 2), exact in FP16."""
+    return torch.randint(1024, 2048, shape, generator=torch.Generator().manual_seed(seed)).double() / 1024
+
+
+def adapter(dg, x, a, b, scale=None, out=F32):
+    """dg_lora of one adapter for all rows, without a base; x, a, b in 64 bits, exact in FP16."""
+    x, a, b = (t.to(F16).to(DEV) for t in (x, a, b))
+    off, pos, slot = dg.dg_route_sort(torch.zeros(x.shape[0], 1, dtype=torch.int32, device=DEV), 1)
+    gs = None if scale is None else torch.tensor([scale], device=DEV)
+    return dg.dg_lora(x, a[None], b[None], off, pos, slot, gs, out=torch.empty(x.shape[0], b.shape[0], dtype=out, device=DEV)).cpu().double()
+
+
+@pytest.mark.parametrize("rank", [24, 32, 72])
+@pytest.mark.parametrize("tokens", [5, 200])
+def test_small_elements_of_an_fp16_row(dg, tokens, rank):
+    """Every element of x A^T alone in an output, 22 bits each, from the row's largest to 2^-23 of it and below."""
+    # v[t, r] = 2^(15 - r) (m0 + 2^-11 m1), the largest at rank 0; ranks from 30 on are zero
+    live = 30 if rank > 30 else rank
+    m = mantissas(rank + tokens, tokens, 2, live)
+    down = 2.0 ** -torch.arange(live).double()
+    x, a = torch.zeros(tokens, 2 * rank + 16, dtype=torch.float64), torch.zeros(rank, 2 * rank + 16, dtype=torch.float64)
+    half = down.sqrt().log2().floor().exp2()  # the way down is shared by x and A
+    x[:, 0 : 2 * live : 2], x[:, 1 : 2 * live : 2] = m[:, 0] * half * 2.0 ** 7, m[:, 1] * half * 2.0 ** 7
+    rest = down / half * 2.0 ** 8
+    for r in range(live):
+        a[r, 2 * r], a[r, 2 * r + 1] = rest[r], rest[r] * 2.0 ** -11
+    for t in (x, a):
+        assert torch.equal(t.to(F16).double(), t)
+    want = torch.zeros(tokens, rank, dtype=torch.float64)
+    want[:, :live] = x @ a[:live].t()
+    say("small elements of %d FP16 rows, rank %d" % (tokens, rank))
+    got = adapter(dg, x, a, torch.eye(rank).double())
+    # A row is scaled to a largest element in [2^14, 2^15). The first FP16 number is within 2^-11 of an element, the second
+    # within 2^-11 of what is left or, where it is subnormal, half a step of 2^-24: 2^-25 / 2^14 of the largest. Both products
+    # with one are exact, their FP32 sum rounds once.
+    top = want.abs().amax(1, keepdim=True)
+    bound = torch.maximum(2.0 ** -22 * want.abs(), 2.0 ** -39 * top) + ref.U32 * 1.01 * want.abs()
+    assert ((got - want).abs() <= bound).all()
+    # what dg_lora promises: 16 bits of every element of at least 2^-23 of its row's largest
+    held = want.abs() >= 2.0 ** -23 * top
+    assert int(held.sum()) >= 23 * tokens and ((got - want).abs() <= 2.0 ** -16 * 1.01 * want.abs())[held].all()
