@@ -355,7 +355,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
   constexpr int TERMS = XK == 1 && OK == 0 ? 3 : 2;
   __shared__ __attribute__((aligned(16))) uint16_t term[TERMS][BM][LD];
   constexpr int LDP = kStrip + 4;  // pitch of a strip's sums in floats
-  __shared__ float back[BM];
+  __shared__ int back[BM];  // exponents of the rows' scaling
   __shared__ int tokens[BM];
   __shared__ __attribute__((aligned(16))) float sums[kWaves][16][LDP];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
@@ -429,21 +429,22 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
       const int m = (i * kThreads + threadIdx.x) / FOURS;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[i][e] *= scale;
-      float down = 1.0f;
       if constexpr (XK == 2) {
         float top = 0.0f;  // of those that are finite
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[i][e]) < __builtin_inff() ? fabsf(v[i][e]) : 0.0f);
 #pragma unroll
         for (int d = 1; d < FOURS; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-        const int e = min(max(__builtin_amdgcn_frexp_expf(top), -100), 100);
-        down = __builtin_amdgcn_ldexpf(1.0f, 15 - e);  // rank 128 and B at its largest: sums below 2^39
-        if (n == 0 && m < BM) back[m] = __builtin_amdgcn_ldexpf(1.0f, e - 15);
+        const int up = 15 - __builtin_amdgcn_frexp_expf(top);  // rank 128 and B at its largest: sums below 2^39
+        // by exponent: 2^up itself may be past FP32's range
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = __builtin_amdgcn_ldexpf(v[i][e], up);
+        if (n == 0 && m < BM) back[m] = -up;
       }
       if (m < BM) {
         uint16_t f[4][TERMS];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split16<XK, TERMS>(v[i][e] * down, f[e]);
+        for (int e = 0; e < 4; ++e) split16<XK, TERMS>(v[i][e], f[e]);
 #pragma unroll
         for (int k = 0; k < TERMS; ++k)
           *reinterpret_cast<uint2*>(&term[k][m][n]) = make_uint2(f[0][k] | ((unsigned)f[1][k] << 16), f[2][k] | ((unsigned)f[3][k] << 16));
@@ -482,7 +483,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
         for (int e = 0; e < PER; e += 4) {
           const v4f f = *reinterpret_cast<const v4f*>(&sums[wave][r][col + e]);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) d[e + v] = XK == 2 ? f[v] * back[m * 16 + r] : f[v];
+          for (int v = 0; v < 4; ++v) d[e + v] = XK == 2 ? __builtin_amdgcn_ldexpf(f[v], back[m * 16 + r]) : f[v];
         }
         if (tok >= 0) add_store<OK>(p, tok, n0 + col, d, old[m][it]);
       }

@@ -62,3 +62,22 @@ def test_small_elements_of_an_fp16_row(dg, tokens, rank):
     # what dg_lora promises: 16 bits of every element of at least 2^-23 of its row's largest
     held = want.abs() >= 2.0 ** -23 * top
     assert int(held.sum()) >= 23 * tokens and ((got - want).abs() <= 2.0 ** -16 * 1.01 * want.abs())[held].all()
+
+
+@pytest.mark.parametrize("tokens", [5, 200])
+@pytest.mark.parametrize("xe,ae,se,be", [(-14, -10, -101, 0), (-14, -10, -102, 3), (14, 14, 90, -14), (14, 14, 95, -12), (0, 0, 0, 0)])
+def test_scales_near_the_ends_of_fp32(dg, tokens, xe, ae, se, be):
+    """x A^T times the adapter's scale is held where FP32 holds it, far outside FP16's range."""
+    rank = 16
+    m = mantissas(tokens, tokens, 2, rank)
+    x, a = torch.zeros(tokens, 64, dtype=torch.float64), torch.zeros(rank, 64, dtype=torch.float64)
+    x[:, 0:32:2], x[:, 1:32:2] = m[:, 0] * 2.0 ** xe, m[:, 1] * 2.0 ** xe
+    for r in range(rank):
+        a[r, 2 * r], a[r, 2 * r + 1] = 2.0 ** ae, 2.0 ** (ae - 11)
+    b = torch.eye(rank).double() * 2.0 ** be
+    want = 2.0 ** se * (x @ a.t()) * 2.0 ** be
+    say("scale 2^%d of products 2^%d" % (se, xe + ae))
+    got = adapter(dg, x, a, b, scale=2.0 ** se)
+    # elements within a factor of two of the row's largest: both numbers normal, 2^-22; the sum rounds once, in FP32's normal
+    # range (2^-126 and more)
+    assert float(want.abs().min()) >= 2.0 ** -126 and ((got - want).abs() <= (2.0 ** -22 + ref.U32) * 1.01 * want.abs()).all()
