@@ -299,8 +299,8 @@ __device__ __forceinline__ void add_store(const LoraArgs& p, int64_t tok, int64_
   }
 }
 
-// A token without an adapter, where out is not base: a wave, which looks at
-// kCopyTokens, copies its row.
+// A token without an adapter (its position is no row's), where out is not base: a
+// wave, which looks at kCopyTokens, copies its row.
 constexpr int kCopyTokens = 8;
 
 template <int OK>
@@ -362,7 +362,8 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
   if (blockIdx.x >= tile_wgs) {
     for (int64_t t0 = ((int64_t)(blockIdx.x - tile_wgs) * kWaves + wave) * kCopyTokens; t0 < p.tokens;
          t0 += (int64_t)(gridDim.x - tile_wgs) * kWaves * kCopyTokens) {
-      uint64_t m = __ballot(lane < kCopyTokens && t0 + lane < p.tokens && p.position[t0 + lane] < 0);
+      const int row = lane < kCopyTokens && t0 + lane < p.tokens ? p.position[t0 + lane] : 0;
+      uint64_t m = __ballot(row < 0 || row >= p.tokens);
       for (; m; m &= m - 1) copy_row<OK>(p, t0 + __builtin_ctzll(m), lane);
     }
     return;

@@ -81,3 +81,24 @@ def test_scales_near_the_ends_of_fp32(dg, tokens, xe, ae, se, be):
     # elements within a factor of two of the row's largest: both numbers normal, 2^-22; the sum rounds once, in FP32's normal
     # range (2^-126 and more)
     assert float(want.abs().min()) >= 2.0 ** -126 and ((got - want).abs() <= (2.0 ** -22 + ref.U32) * 1.01 * want.abs()).all()
+
+
+@pytest.mark.parametrize("with_base", [True, False])
+@pytest.mark.parametrize("tokens,groups", [(20, 3), (300, 2)])
+def test_positions_outside_have_no_adapter(dg, tokens, groups, with_base):
+    """A row whose position is not in 0 .. tokens - 1 is base alone, whatever the value."""
+    K, N, rank = 128, 70, 16
+    gen = torch.Generator().manual_seed(tokens)
+    r = lambda *shape: torch.randn(*shape, generator=gen).to(BF16).to(DEV)  # noqa: E731
+    x, a, b, base = r(tokens, K), r(groups, rank, K), r(groups, N, rank), r(tokens, N) if with_base else None
+    ids = (torch.arange(tokens, dtype=torch.int32) % groups)[:, None]
+    ids[::4] = -1
+    off, pos, slot = dg.dg_route_sort(ids.to(DEV), groups)
+    say("positions outside, %d tokens base=%d" % (tokens, with_base))
+    want = dg.dg_lora(x, a, b, off, pos, slot, None, base, torch.full((tokens, N), -99.0, dtype=BF16, device=DEV))
+    assert torch.equal(want[::4], torch.zeros_like(want[::4]) if base is None else base[::4])
+    for value in (tokens, tokens + 1, 1 << 30, (1 << 31) - 1, -(1 << 31)):
+        other = pos.clone()
+        other[::4] = value
+        out = torch.full((tokens, N), -99.0, dtype=BF16, device=DEV)
+        assert torch.equal(dg.dg_lora(x, a, b, off, other, slot, None, base, out), want), value
