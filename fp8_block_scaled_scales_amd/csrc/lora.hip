@@ -327,13 +327,14 @@ __device__ __forceinline__ float rest_of(float f, float h) {
 }
 
 // f as TERMS 16-bit numbers: its rounding, that of the rest, ... (an infinite one
-// has no rest)
+// has no rest; a finite one that BF16 would round to infinity leaves what is past
+// the largest BF16 to its rest)
 template <int XK, int TERMS>
 __device__ __forceinline__ void split16(float f, uint16_t (&t)[TERMS]) {
 #pragma unroll
   for (int i = 0; i < TERMS; ++i) {
     if constexpr (XK == 1) {
-      const __bf16 h = (__bf16)f;
+      const __bf16 h = (__bf16)(fabsf(f) < __builtin_inff() ? fminf(fmaxf(f, -0x1.fep127f), 0x1.fep127f) : f);
       t[i] = __builtin_bit_cast(uint16_t, h);
       f = rest_of(f, (float)h);
     } else {

@@ -102,3 +102,26 @@ def test_positions_outside_have_no_adapter(dg, tokens, groups, with_base):
         other[::4] = value
         out = torch.full((tokens, N), -99.0, dtype=BF16, device=DEV)
         assert torch.equal(dg.dg_lora(x, a, b, off, other, slot, None, base, out), want), value
+
+
+@pytest.mark.parametrize("ok", [F32, BF16])
+@pytest.mark.parametrize("tokens", [5, 200])
+def test_products_between_the_largest_bf16_and_fp32(dg, tokens, ok):
+    """Finite elements of x A^T that round to an infinity in BF16 stay finite in out where the formula's sum is."""
+    x, a = torch.zeros(tokens, 64, dtype=BF16), torch.zeros(1, 8, 64, dtype=BF16)
+    big = torch.finfo(BF16).max  # 3.39e38
+    x[:, 0], x[:, 1], a[0, :, 0] = big, 1.0, 1.0
+    for r, v in enumerate((1.0, 6e35, 7e35, 1e36, 1.2e36, 0.0, 1e30, 6.7e35)):  # half a step past the largest is 6.65e35
+        a[0, r, 1] = v
+    x[1::3] *= -1
+    b = torch.zeros(1, 24, 8, dtype=BF16)
+    b[0, :8], b[0, 8:16], b[0, 16:] = torch.eye(8) * 0.5, torch.eye(8) * -0.25, torch.eye(8) * 2.0 ** -100
+    v = x.double() @ a[0].double().t()
+    assert float(v.abs().max()) <= torch.finfo(F32).max
+    off, pos, slot = dg.dg_route_sort(torch.zeros(tokens, 1, dtype=torch.int32, device=DEV), 1)
+    say("products past the largest BF16, %d rows" % tokens)
+    out = dg.dg_lora(x.to(DEV), a.to(DEV), b.to(DEV), off, pos, slot, out=torch.empty(tokens, 24, dtype=ok, device=DEV)).cpu().double()
+    want = v @ b[0].double().t()
+    # two BF16 numbers (2^-16), FP32 roundings of x A^T and of the sum, one of out
+    room = (2.0 ** -16 + 3 * ref.U32 + (0.0 if ok == F32 else ref.half_step(BF16))) * 1.01 * want.abs()
+    assert ((out - want).abs() <= room).all()
