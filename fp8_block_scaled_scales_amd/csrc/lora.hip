@@ -345,6 +345,12 @@ __device__ __forceinline__ void split16(float f, uint16_t (&t)[TERMS]) {
   }
 }
 
+template <int XK>
+__device__ __forceinline__ float widen16(uint16_t h) {
+  if constexpr (XK == 1) return __uint_as_float((unsigned)h << 16);
+  else return (float)__builtin_bit_cast(_Float16, h);
+}
+
 // out of MT x 16 rows by `strips` x 4 x 64 columns. The rows of B_l are the
 // first operand: a lane's four sums are neighbours in a token's row, and pass
 // through LDS (16 tokens of a strip at a time, a wave's own) to lanes that hold 16
@@ -359,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
   __shared__ int back[BM];  // exponents of the rows' scaling
   __shared__ int tokens[BM];
   __shared__ __attribute__((aligned(16))) float sums[kWaves][16][LDP];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
+  int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, q = lane >> 4;
   if (blockIdx.x >= tile_wgs) {
     for (int64_t t0 = ((int64_t)(blockIdx.x - tile_wgs) * kWaves + wave) * kCopyTokens; t0 < p.tokens;
          t0 += (int64_t)(gridDim.x - tile_wgs) * kWaves * kCopyTokens) {
@@ -383,13 +389,11 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
   const uint16_t* const b = static_cast<const uint16_t*>(p.b) + (int64_t)t.group * p.N * p.rank;
   // a lane's outputs: PER columns from col on, of tokens RPI apart
   constexpr int PER = Out16<OK>::PER, LPR = kStrip / PER, RPI = 64 / LPR, ITS = 16 / RPI;
-  const int col = (lane % LPR) * PER, row = lane / LPR;
+  int col = (lane % LPR) * PER, row = lane / LPR;
   auto first_col = [&](int st) { return (((int64_t)t.tn * strips + st) * kWaves + wave) * kStrip; };
   v4u br[KS][4];
   unsigned old[MT][ITS][PER];
-  // A strip's rows of B_l and all of its base, ahead of the first store, which may
-  // be to the same memory.
-  auto load = [&](int64_t n0) {
+  auto load_b = [&](int64_t n0) {  // a strip's rows of B_l
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -399,6 +403,8 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
         const int64_t n = min(n0 + 16 * s + i16, p.N - 1);
         br[ks][s] = *reinterpret_cast<const v4u*>(b + n * p.rank + min(32 * ks + 8 * q, p.rank - 8));
       }
+  };
+  auto load_bases = [&](int64_t n0) {  // all of its base, ahead of the first store, which may be to the same memory
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -406,6 +412,40 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
         const int tok = tokens[m * 16 + it * RPI + row];
         if (tok >= 0) load_base<OK>(p, tok, n0 + col, old[m][it]);
       }
+  };
+
+  // the strip's sums of 16 tokens, to LDS
+  auto sums_of = [&](int m) {
+    v4f acc[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) acc[s] = (v4f){};
+#pragma unroll
+    for (int k = TERMS - 1; k >= 0; --k)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const v4u h = *reinterpret_cast<const v4u*>(&term[k][m * 16 + i16][32 * ks + 8 * q]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) acc[s] = mfma16x32<XK>(br[ks][s], h, acc[s]);
+      }
+    // a wave's LDS operations are in order: no barrier, but none may be moved
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) *reinterpret_cast<v4f*>(&sums[wave][i16][16 * s + 4 * q]) = acc[s];
+    __builtin_amdgcn_wave_barrier();
+  };
+  // a lane's sums of one of them; whether none is NaN (nor infinities of both signs among them)
+  auto sums_at = [&](int m, int r, float (&d)[PER]) {
+    float all = 0.0f;
+#pragma unroll
+    for (int e = 0; e < PER; e += 4) {
+      const v4f f = *reinterpret_cast<const v4f*>(&sums[wave][r][col + e]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        d[e + v] = XK == 2 ? __builtin_amdgcn_ldexpf(f[v], back[m * 16 + r]) : f[v];
+        all += f[v];
+      }
+    }
+    return all == all;
   };
 
   // v of the tile, its terms to LDS: neighbouring threads take neighbouring fours
@@ -455,39 +495,84 @@ __global__ __launch_bounds__(kThreads) void lora_expand(const LoraArgs p, const 
   }
   __syncthreads();
 
+  bool again = false;
   for (int st = 0; st < strips; ++st) {
     const int64_t n0 = first_col(st);
-    if (n0 >= p.N) return;
-    load(n0);  // ahead of v instead: 42.9 -> 45 us
+    if (n0 >= p.N) break;
+    load_b(n0);  // ahead of v instead: 42.9 -> 45 us
+    load_bases(n0);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      v4f acc[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) acc[s] = (v4f){};
-#pragma unroll
-      for (int k = TERMS - 1; k >= 0; --k)
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const v4u h = *reinterpret_cast<const v4u*>(&term[k][m * 16 + i16][32 * ks + 8 * q]);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) acc[s] = mfma16x32<XK>(br[ks][s], h, acc[s]);
-        }
-      // a wave's LDS operations are in order: no barrier, but none may be moved
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int s = 0; s < 4; ++s) *reinterpret_cast<v4f*>(&sums[wave][i16][16 * s + 4 * q]) = acc[s];
-      __builtin_amdgcn_wave_barrier();
+      sums_of(m);
 #pragma unroll
       for (int it = 0; it < ITS; ++it) {
         const int r = it * RPI + row, tok = tokens[m * 16 + r];
         float d[PER];
+        const bool whole = sums_at(m, r, d);
+        if (tok >= 0 && whole) add_store<OK>(p, tok, n0 + col, d, old[m][it]);
+        again |= tok >= 0 && !whole;
+      }
+    }
+  }
+  if (!__any(again)) return;
+
+  // Outputs with a NaN among their sums, which were left as they were. An infinite
+  // element of B is NaN times the rest of an element of v that has none, or of the
+  // other sign, and times the zeros past the rank: where B holds one, sums that came
+  // out NaN are taken again, element by element. (The lane's numbers are worked out
+  // anew, so that none is held in a register until here: 8192 x 4096 to 4096 at rank
+  // 128, eight adapters, 102 -> 93 us.)
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  lane = tid & 63, wave = tid >> 6, i16 = lane & 15, q = lane >> 4;
+  col = (lane % LPR) * PER, row = lane / LPR;
+  for (int st = 0; st < strips; ++st) {
+    const int64_t n0 = first_col(st);
+    if (n0 >= p.N) return;
+    load_b(n0);
+    v2u16 top = {};
 #pragma unroll
-        for (int e = 0; e < PER; e += 4) {
-          const v4f f = *reinterpret_cast<const v4f*>(&sums[wave][r][col + e]);
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) d[e + v] = XK == 2 ? __builtin_amdgcn_ldexpf(f[v], back[m * 16 + r]) : f[v];
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, abs_bits2(br[ks][s][i]));
+    const bool beyond = __any(max(top.x, top.y) >= (XK == 1 ? 0x7F80 : 0x7C00));
+#pragma unroll 1
+    for (int m = 0; m < MT; ++m) {
+      sums_of(m);
+      unsigned left = 0;  // this lane's outputs that were left
+#pragma unroll 1
+      for (int it = 0; it < ITS; ++it) {
+        float d[PER];
+        left |= (unsigned)!sums_at(m, it * RPI + row, d) << it;
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+      for (int i = 0; beyond && i < 16; ++i) {
+        const int c = 16 * (i >> 2) + 4 * q + (i & 3);
+        if (n0 + c >= p.N || sums[wave][i16][c] == sums[wave][i16][c]) continue;
+        const uint16_t* const bn = b + (n0 + c) * p.rank;
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int r = 0; r < p.rank; ++r) {
+          float f = 0.0f;
+#pragma unroll
+          for (int k = TERMS - 1; k >= 0; --k) f += widen16<XK>(term[k][m * 16 + i16][r]);
+          sum = __builtin_fmaf(f, widen16<XK>(bn[r]), sum);
         }
-        if (tok >= 0) add_store<OK>(p, tok, n0 + col, d, old[m][it]);
+        sums[wave][i16][c] = sum;
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+      for (int it = 0; it < ITS; ++it) {
+        const int r = it * RPI + row, tok = tokens[m * 16 + r];
+        if (tok < 0 || !(left >> it & 1)) continue;
+        float d[PER];
+        unsigned w[PER];
+        sums_at(m, r, d);
+        load_base<OK>(p, tok, n0 + col, w);
+        add_store<OK>(p, tok, n0 + col, d, w);
       }
     }
   }

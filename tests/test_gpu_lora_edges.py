@@ -125,3 +125,41 @@ def test_products_between_the_largest_bf16_and_fp32(dg, tokens, ok):
     # two BF16 numbers (2^-16), FP32 roundings of x A^T and of the sum, one of out
     room = (2.0 ** -16 + 3 * ref.U32 + (0.0 if ok == F32 else ref.half_step(BF16))) * 1.01 * want.abs()
     assert ((out - want).abs() <= room).all()
+
+
+@pytest.mark.parametrize("xk", [BF16, F16])
+@pytest.mark.parametrize("ok", [F32, BF16])
+@pytest.mark.parametrize("tokens,rank", [(5, 8), (5, 32), (200, 16), (200, 72), (150, 128)])
+def test_infinities_in_b(dg, tokens, rank, xk, ok):
+    """An infinite or NaN element of B_l makes of its output what the formula does; other outputs keep their bits."""
+    N, K = 203, 256
+    gen = torch.Generator().manual_seed(rank)
+    x, a = torch.zeros(tokens, K, dtype=xk), torch.zeros(1, rank, K, dtype=xk)
+    whole = torch.randint(1, 200, (tokens, rank), generator=gen).double() * (1 - 2 * torch.randint(0, 2, (tokens, rank), generator=gen))
+    x[:, :rank] = whole.to(xk)
+    x[:, rank : 2 * rank] = (whole / 512).to(xk)
+    x[3, :rank] = 0
+    x[3, rank : 2 * rank] = 0  # no product but zero: an infinity times it is NaN
+    x[2, 1] = x[2, rank + 1] = 0
+    for r in range(rank):
+        a[0, r, r] = a[0, r, rank + r] = 1.0  # 8 and more bits: the second numbers are zero for some, of either sign for others
+    b = torch.randn(1, N, rank, generator=gen).to(xk)
+    bad = b.clone()
+    inf = float("inf")
+    bad[0, 7, 0], bad[0, 64, rank - 1], bad[0, 65, 2], bad[0, 130, 1], bad[0, 202, 3] = inf, -inf, float("nan"), inf, -inf
+    bad[0, 131, 4], bad[0, 131, 5] = inf, inf  # two of them: NaN where their products' signs differ
+    base = torch.randn(tokens, N, generator=gen).to(ok)
+    off, pos, slot = dg.dg_route_sort(torch.zeros(tokens, 1, dtype=torch.int32, device=DEV), 1)
+    say("infinities in B, %d rows of rank %d %s %s" % (tokens, rank, xk, ok))
+    clean, out = (dg.dg_lora(x.to(DEV), a.to(DEV), t.to(DEV), off, pos, slot, None, base.to(DEV)).cpu() for t in (b, bad))
+    v = x.double() @ a[0].double().t()
+    want = base.double() + (v[:, None] * bad[0].double()[None]).sum(2)
+    finite = torch.isfinite(want)
+    assert torch.isfinite(out[finite]).all() and torch.equal(out[finite], clean[finite])
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.double()[torch.isinf(want)], want[torch.isinf(want)])
+    over = base.to(DEV)
+    dg.dg_lora(x.to(DEV), a.to(DEV), bad.to(DEV), off, pos, slot, None, over, over)  # in place
+    bits = {F32: torch.int32, BF16: torch.int16}[ok]
+    assert torch.equal(over.cpu().view(bits), out.view(bits))
+    assert int(torch.isinf(want).sum()) > 2 * tokens and torch.isnan(want[3, 7])
