@@ -820,6 +820,12 @@ def _count(n, name):
     return n
 
 
+def _sizes(name, *sizes):
+    """Refuses sizes that no call takes: ctypes would hand the library what is left of them in a C integer."""
+    if any(n < 0 or n > DG_MAX_DIM for n in sizes):
+        _raise(DG_EINVAL, name)
+
+
 def _groups(offsets, dev):
     """The number of groups that an offsets array is for."""
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 2 <= offsets.shape[0] <= DG_MAX_GROUPS + 1:
@@ -848,6 +854,7 @@ def dg_route_sort(ids, groups: int, align: int = 1, offsets=None, position=None,
     tokens, k = shape = _matrix(ids, "ids")
     dev = ids.device
     _check(ids, "ids", tuple(_ID_BYTES), shape, dev)
+    _sizes("dg_route_sort", tokens, k, groups, align)
     least = _count(_lib.dg_route_rows(tokens, k, groups, align), "dg_route_sort")
     if slot is not None and (not isinstance(slot, torch.Tensor) or slot.dim() != 1 or slot.shape[0] < least):
         raise ValueError("slot must be 1-D with at least dg_route_rows(...) = %d entries" % least)
@@ -864,11 +871,13 @@ def dg_route_sort(ids, groups: int, align: int = 1, offsets=None, position=None,
 
 def dg_route_rows(tokens: int, k: int, groups: int, align: int = 1) -> int:
     """Sorted rows that hold any routing of tokens x k choices among groups."""
+    _sizes("dg_route_rows", tokens, k, groups, align)
     return _count(_lib.dg_route_rows(tokens, k, groups, align), "dg_route_rows")
 
 
 def dg_route_sort_workspace(tokens: int, k: int, groups: int) -> int:
     """Workspace bytes of dg_route_sort."""
+    _sizes("dg_route_sort_workspace", tokens, k, groups)
     return _count(_lib.dg_route_sort_workspace(tokens, k, groups), "dg_route_sort_workspace")
 
 
@@ -914,6 +923,7 @@ def dg_route_quantize_fp8(x, position, slot, weights=None, gran: int = 128, bloc
         raise ValueError("block_rows must be gran (g x g blocks) or 1 (per-row factors)")
     if fmt not in _FP8_OF:
         raise ValueError("fmt must be DG_FMT_E4M3 or DG_FMT_E5M2")
+    _sizes("dg_route_quantize_fp8", tokens, cols, k, rows)
     ldx = _rows(x, "x", _IN_OF, (tokens, cols), dev)
     q = _out(q, "q", _FP8_OF[fmt], (rows, cols), dev, stream)
     scales = _out(scales, "scales", _F32, ((rows + block_rows - 1) // block_rows, cols // gran), dev, stream)
@@ -927,6 +937,7 @@ def dg_route_quantize_fp8(x, position, slot, weights=None, gran: int = 128, bloc
 
 def dg_route_quantize_workspace(tokens: int, cols: int, k: int, rows: int, gran: int = 128, block_rows: int = 1) -> int:
     """Workspace bytes of dg_route_quantize_fp8."""
+    _sizes("dg_route_quantize_workspace", tokens, cols, k, rows, gran, block_rows)
     return _count(_lib.dg_route_quantize_workspace(tokens, cols, k, rows, gran, block_rows), "dg_route_quantize_workspace")
 
 
@@ -949,6 +960,7 @@ def dg_route_combine(y, position, weights=None, res=None, out=None, stream=None)
     dev = y.device
     if not rows or not tokens or not k or cols % 8 or not cols:
         raise ValueError("y must have rows, and columns in a multiple of 8; position must have entries")
+    _sizes("dg_route_combine", rows, tokens, cols, k)
     _check(position, "position", _I32, (tokens, k), dev)
     if weights is not None:
         _check(weights, "weights", _F32, (tokens, k), dev)
@@ -981,6 +993,7 @@ def dg_route_weight_grad(dout, y, position, dweights=None, stream=None):
     k = _matrix(position, "position")[1]
     if not rows or not tokens or not k or cols % 8 or not cols:
         raise ValueError("dout and y must have rows, and columns in a multiple of 8; position must have entries")
+    _sizes("dg_route_weight_grad", rows, tokens, cols, k)
     _check(position, "position", _I32, (tokens, k), dev)
     ldd = _rows(dout, "dout", _IN_OF, (tokens, cols), dev)
     ldy = _rows(y, "y", _IN_OF, (rows, cols), dev)
@@ -1098,6 +1111,7 @@ def dg_lora(x, a, b, offsets, position, slot, scale=None, base=None, out=None, w
     rank, N = a.shape[1], b.shape[1]
     _check(a, "a", (x.dtype,), (groups, rank, K), dev)
     _check(b, "b", (x.dtype,), (groups, N, rank), dev)
+    _sizes("dg_lora", tokens, K, N, rank)
     need = _count(_lib.dg_lora_workspace(tokens, K, N, rank, groups), "dg_lora")
     _check(position, "position", _I32, (tokens, 1), dev)
     _check(slot, "slot", _I32, (tokens,), dev)
@@ -1117,6 +1131,7 @@ def dg_lora(x, a, b, offsets, position, slot, scale=None, base=None, out=None, w
 
 def dg_lora_workspace(tokens: int, K: int, N: int, rank: int, adapters: int) -> int:
     """Workspace bytes of dg_lora."""
+    _sizes("dg_lora_workspace", tokens, K, N, rank, adapters)
     return _count(_lib.dg_lora_workspace(tokens, K, N, rank, adapters), "dg_lora_workspace")
 
 
