@@ -13,9 +13,11 @@
 // the accesses, since the instruction's layout gives neighbouring lanes
 // neighbouring rows: there the first product's operands pass through LDS. The
 // outputs always do, so that neighbouring lanes hold neighbouring columns. 64 rows of
-// 128 adapters, 7168 to 4096 at rank 16: 5.6 + 6.5 us (19 MB: 3); 8192 of 8, 4096 to
-// 4096 at rank 64: 25 + 44 us (0.21 GB: 36), the first at the rate at which a CU
-// keeps lines in flight, the second with every output through LDS (49 straight).
+// 128 adapters, 7168 to 4096 at rank 16: 5.6 + 6.5 us (19 MB: 3), each a launch and a
+// chain of offsets, slots and operands; 8192 of 8, 4096 to 4096 at rank 64: 25 + 45 us
+// (0.21 GB: 36), the first 136 tiles in three parts on CUs that hold two workgroups (152
+// CUs have two, 104 one), the second with every output through LDS (49 straight), the
+// partial sums of v, then a strip's B and base waited for before its stores.
 //
 // Rounding: v is FP32; it enters the second product as the sum of two 16-bit
 // numbers (its rounding and that of the rest, 16 bits of BF16 or 22 of FP16),

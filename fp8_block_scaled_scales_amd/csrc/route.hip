@@ -31,8 +31,8 @@ namespace {
 constexpr int kMaxGroups = 1024;  // the library's DG_MAX_GROUPS
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 
-// Slots that one workgroup sorts alone (sort and dispatch of 4096 slots 13.3 us, of
-// 8192 16.0, and in chunks 15.1 and 15.1); beyond, chunks of at least kChunk slots,
+// Slots that one workgroup sorts alone (calls of 2048, 4096 and 8192 slots 5.6, 7.0
+// and 10.2 us, in chunks 8.3, 8.3 and 8.5); beyond, chunks of at least kChunk slots,
 // at most 256 of them, are counted by one launch and placed by a second.
 constexpr int64_t kOneSort = 4096, kChunk = 1024;
 
@@ -296,12 +296,11 @@ struct Piece {
 // columns. OWN: 1 x g, the factors are the token's own segments' (with weights:
 // each row's, since |w x| is largest where |x| is: rounding keeps order);
 // otherwise the factors of g x g blocks are in scales already. Sorted rows taken
-// by their own waves instead would read x k times. 69 us (0.34 GB: 57; with two
-// corrections of every quotient 78, the vector ALU busy 84% of the cycles), with
-// weights, whose quotients need both, 94; 1 x
-// g, 2000 x 2 rows of 7168 in FP32 with weights 22 (86 MB: 15; 33 while a wave cleared
-// up to 64 rows between groups; sharing the factors' divisions over a segment's
-// lanes changed nothing).
+// by their own waves instead would read x k times. 69 us (0.34 GB: 57; the vector ALU
+// busy 79% of the cycles; with two corrections of every quotient 78 us), with weights,
+// whose quotients need both, 94 (84%); 1 x g, 2000 x 2 rows of 7168 in FP32 with
+// weights 22.5 (86 MB: 15; 33 while a wave cleared up to 64 rows between groups;
+// sharing the factors' divisions over a segment's lanes changed nothing).
 template <int XK, bool W, bool OWN, int U, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void route_rows(const RouteQuantArgs p, int pieces, int token_wgs) {
   constexpr int E = unit_of(XK, 1);
@@ -417,7 +416,8 @@ __global__ __launch_bounds__(kRowThreads) void route_maxima(const RouteQuantArgs
 // The factors of g x g blocks of sorted rows from the tokens' maxima, and their
 // reciprocals (behind the maxima) for the many divisions that follow: a
 // workgroup takes a row of blocks, 32 of them, its threads 32 rows at a time. 9.1 us,
-// the latency of slot, then maximum, four times over.
+// the latency of slot, then maximum, four times over: a load stays under the test of
+// its index, and is waited for there before the next.
 constexpr int kFactorThreads = 1024;
 
 template <bool W>
@@ -453,7 +453,9 @@ __global__ __launch_bounds__(kFactorThreads) void route_factors(const RouteQuant
 }
 
 // g x g: one block of sorted rows per workgroup, its values in registers between
-// amax and codes. 4096 x 2 rows of 7168 at g = 128: 55 us with the sort (0.18 GB: 30).
+// amax and codes. 4096 x 2 rows of 7168 at g = 128: 54 us with the sort (0.18 GB: 30).
+// A pass loads its slot, then its row, and each is waited for before the next pass's:
+// eight trips in a row before the maximum.
 template <int XK, int G, int NT, bool W>
 __global__ __launch_bounds__(NT) void route_blocks(const RouteQuantArgs p) {
   constexpr int E = 8, ROW_L = G / E, RPP = NT / ROW_L, PASSES = G / RPP;
@@ -507,17 +509,21 @@ constexpr int64_t kMaxWgs = 1 << 20;
 
 // g x g blocks by tokens: three launches that read every token twice, instead of
 // one that gathers every row of a block (and reads it twice). It pays where a
-// token has several rows and the codes are many. Sort and dispatch of BF16 rows,
-// by tokens / by blocks, in us: 1024 x 8 of 4096 41 / 32, 2048 x 8 of 4096 42 /
-// 48, 8192 x 8 of 4096 109 / 163; 4096 x 2 of 7168 72 / 55, 8192 x 2 of 7168 106 /
-// 94, 4096 x 4 of 7168 80 / 82, 16384 x 2 of 4096 102 / 105.
+// token has several rows and the codes are many; rows are those allocated, since the
+// host does not know how many of them groups have, and those between groups are
+// cleared by either. Sort and dispatch of BF16 rows to groups of 128, by tokens / by
+// blocks, in us: 1024 x 8 of 4096 to 64 groups 33.0 / 31.2, 2048 x 8 44.5 / 48.2, 8192 x 8
+// 95 / 160; 4096 x 2 of 7168 to 8 61.5 / 53.8, 8192 x 2 87 / 93, 16384 x 2 of 4096 93 / 104;
+// 4096 x 4 of 7168 to 16 64 / 81; 64 x 8 of 8192 to 64, of whose rows most are between
+// groups, 24.7 / 26.4.
 constexpr int64_t kByTokens = 1ll << 26;
 
 bool by_tokens(int64_t tokens, int64_t rows, int64_t cols) { return (rows - tokens) * cols >= kByTokens; }
 
 // Units per lane: four where that leaves the chip enough waves (32 a CU). Sort and
-// dispatch to 1 x g, one / four, in us: 1024 x 2 of 4096 in BF16 12.0 / 13.9, 2000 x
-// 2 of 7168 20.2 / 22.5, in FP32 30.9 / 25.5; 8192 x 2 of 4096 to g x g 75 / 67.
+// dispatch to 1 x g, one / four, in us: 1024 x 2 of 4096 in BF16 12.5 / 12.5, 2000 x
+// 2 of 7168 20.4 / 22.5, in FP32 28.8 / 25.6; 8192 x 2 of 4096 42.9 / 43.8, to g x g
+// 57.9 / 57.8.
 template <int E>
 int units_per_lane(int64_t tokens, int64_t cols) {
   return cols >= 64 * E * 4 && tokens * (cols / (64 * E * 4)) >= 8192 ? 4 : 1;
@@ -539,7 +545,7 @@ hipError_t launch_tokens(const RouteQuantArgs& p, hipStream_t stream) {
     if (err != hipSuccess) return err;
   }
   const dim3 grid((unsigned)(pieces * tokens + pads));
-  // past the caches: 8192 x 8 of 4096 to 1 x g 83 -> 78 us, 2048 x 8 25.1 -> 26.3
+  // past the caches: 8192 x 8 of 4096 to 1 x g 82 -> 78 us, 4096 x 8 48 -> 44, 2048 x 8 25.2 -> 27.8
   if (p.rows * p.cols + p.tokens * p.cols * InKind<XK>::kBytes >= 2 * kOnceBytes)
     hipLaunchKernelGGL((route_rows<XK, W, OWN, U, true>), grid, dim3(kRowThreads), 0, stream, p, (int)pieces, (int)tokens);
   else
@@ -566,8 +572,10 @@ hipError_t launch_rows(const RouteQuantArgs& p, hipStream_t stream) {
 
 // ---- the combine --------------------------------------------------------------
 //
-// A thread takes 16 bytes of out and the same columns of its token's k rows, four
-// loads in flight. 116 us (0.60 GB: 102).
+// A thread takes 16 bytes of out and the same columns of its token's k rows, one
+// after the other: a row's load is under the test of its position and is waited for
+// before the next position's, 2 k trips in a row, which the waves of a large call hide
+// and those of a small one do not. 116 us (0.60 GB: 102); 64 x 8 rows 4.4 (5.2 MB: 0.9).
 
 template <int YK, int OK, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void route_combine(const CombineArgs p, int64_t units) {
@@ -602,7 +610,7 @@ template <int YK, int OK>
 hipError_t launch_combine_k(const CombineArgs& p, hipStream_t stream) {
   const int64_t units = p.tokens * (p.cols / unit_of(YK, OK));
   const int64_t wgs = std::min((units + kRowThreads - 1) / kRowThreads, kMaxWgs);
-  // past the caches: 8192 x 8 rows of 4096 in BF16 123 -> 114 us, 1024 x 8 12.8 -> 16.9
+  // past the caches: 8192 x 8 rows of 4096 in BF16 121 -> 120 us, 2048 x 8 34.4 -> 32.1, 1024 x 8 12.7 -> 17.0
   if (p.tokens * p.k * p.cols * InKind<YK>::kBytes >= 2 * kOnceBytes)
     hipLaunchKernelGGL((route_combine<YK, OK, true>), dim3((unsigned)wgs), dim3(kRowThreads), 0, stream, p, units);
   else
@@ -622,8 +630,9 @@ hipError_t launch_combine_y(const CombineArgs& p, hipStream_t stream) {
 
 // ---- the gradient of the weights ----------------------------------------------
 
-// A workgroup takes a token, eight of its rows at a time: x once per eight rows. 101
-// us (0.60 GB: 102); 2000 x 2 of 7168, x in FP32, 20.4 (115 MB: 19).
+// A workgroup takes a token, eight of its rows at a time: x once per eight rows, whose
+// loads follow one another (the many workgroups' overlap). 101 us (0.60 GB: 102); 2000 x 2
+// of 7168, x in FP32, 20.4 (115 MB: 19).
 template <int XK, int YK, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void route_weight_grad(const WeightGradArgs p) {
   constexpr int E = unit_of(XK, YK), J = 8;
@@ -671,8 +680,8 @@ __global__ __launch_bounds__(kRowThreads) void route_weight_grad(const WeightGra
 template <int XK, int YK>
 hipError_t launch_weight_grad_k(const WeightGradArgs& p, hipStream_t stream) {
   const dim3 grid((unsigned)std::min<int64_t>(p.tokens, kMaxWgs)), block(kRowThreads);
-  // past the caches: with the rows' codes 8192 x 8 of 4096 in BF16 224 -> 203 us, 1024
-  // x 8 45.5 -> 44.1, 512 x 8 34.1 -> 35.7
+  // past the caches: with the rows' codes 8192 x 8 of 4096 in BF16 223 -> 206 us, 1024
+  // x 8 41.9 -> 36.0, 512 x 8 34.1 -> 35.7
   if (p.tokens * p.k * p.cols * InKind<YK>::kBytes >= kOnceBytes)
     hipLaunchKernelGGL((route_weight_grad<XK, YK, true>), grid, block, 0, stream, p);
   else

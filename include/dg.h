@@ -63,7 +63,9 @@ extern "C" {
  * but dg_gemm_fp8_ws splits K over workgroups. 2.1.0: the quantisers take
  * BF16 and FP16 input through the _typed calls. 2.2.0: the RMS norm with FP8
  * output and its backward pass, the product with a residual in its epilogue,
- * and the gradient through that epilogue). */
+ * the gradient through that epilogue, and the calls of layers whose weights each
+ * row chooses, which came later: look up dg_route_sort to know whether they are
+ * there). */
 #define DG_VERSION 220
 
 /* Largest accepted dimension, 2^24 - 256: a 256-row tile of K bytes per row
